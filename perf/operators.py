@@ -197,8 +197,9 @@ def _plain_quant(x, swiglu):
     if swiglu:
         gate, up = v.chunk(2, dim=1)
         v = gate / (1 + torch.exp(-gate)) * up
-    mult = 127 / v.abs().amax(1).clamp_min(2.0 ** -64)
-    return torch.round(v * mult[:, None]), 1 / mult
+    # one division, rounded once (a Python number over a tensor is a reciprocal and a product)
+    mult = v.new_full((), 127.0) / v.abs().amax(1).clamp_min(2.0 ** -64)
+    return torch.round(v * mult[:, None]), mult.reciprocal()
 
 
 def _plain_mm_i8(s, codes, scale):
