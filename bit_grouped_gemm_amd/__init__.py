@@ -18,8 +18,14 @@ Entry points (same names as the C ABI):
     moe_prepack_weights(cfg, weights) -> TiledWeights
     moe_route(cfg, x, gate_w) -> (topk_ids, topk_weights)   (the router in front of the layer)
     moe_encode_e4m3(v) -> codes   (diagnostic: the quantisers' fp32 -> e4m3 conversion)
+and on row-major weights (nothing to prepack):
+    moe_grouped_mm(x, w, offsets) -> y   (bf16 / fp16 experts; differentiable)
+    moe_grouped_mm_dgrad(dy, w, offsets) -> dx,  moe_grouped_mm_wgrad(dy, x, offsets) -> dw
+    moe_quant_i8(x, swiglu=False) -> (codes, scales)   (int8, one scale per token)
+    moe_mm_i8(xq, xs, wq, ws, offsets=None, row_token=None) -> y   (grouped or dense)
+    moe_linear_i8(x, wq, ws, offsets=None, row_token=None, swiglu=False) -> y   (both in one call)
 
-The GEMM entry points read expert weights in the tiled layout: convert the
+The layer's GEMM entry points read expert weights in the tiled layout: convert the
 canonical row-major tensors once with moe_prepack_weights(cfg, weights)
 (a one-time step at weight load).
 """
@@ -52,7 +58,12 @@ EXPORTS = ("moe_workspace_size", "moe_permute", "moe_grouped_gemm1_swiglu", "moe
            "moe_combine", "moe_layer", "moe_layer_static", "moe_layer_persistent", "moe_layer_persistent_spin_limit",
            "moe_prepack_weights",
            "moe_stream_read",
-           "moe_mfma_rate", "moe_encode_e4m3", "moe_route", "moe_route_workspace_size", "moe_status_str")
+           "moe_mfma_rate", "moe_encode_e4m3", "moe_route", "moe_route_workspace_size", "moe_status_str",
+           "moe_grouped_mm", "moe_grouped_mm_dgrad", "moe_grouped_mm_wgrad", "moe_quant_i8", "moe_mm_i8",
+           "moe_linear_i8", "moe_linear_i8_workspace_size")
+
+# element types of the row-major products
+_DT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 class MoeCfg(C.Structure):
@@ -63,6 +74,10 @@ class MoeCfg(C.Structure):
 class MoeWeights(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("w1", "w1s", "w2", "w2s", "sw1", "sw1s", "sw2", "sw2s")] + \
         [("prepacked", C.c_int32)] + [(n, C.c_void_p) for n in ("w1g", "w2g", "sw1g", "sw2g")]
+
+
+class MoeMmCfg(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("R", "N", "K", "E", "T", "dtype", "out_dtype", "clear_tail")]
 
 
 class MoeError(RuntimeError):
@@ -101,6 +116,14 @@ def load(path: str = LIB_PATH) -> C.CDLL:
     L.moe_encode_e4m3.argtypes = [vp, sz, vp, vp]
     L.moe_route_workspace_size.argtypes = [cfgp, C.POINTER(sz)]
     L.moe_route.argtypes = [cfgp, vp, vp, vp, vp, vp, sz, vp]
+    mmp = C.POINTER(MoeMmCfg)
+    L.moe_grouped_mm.argtypes = [mmp, vp, vp, vp, vp, vp]
+    L.moe_grouped_mm_dgrad.argtypes = [mmp, vp, vp, vp, vp, vp]
+    L.moe_grouped_mm_wgrad.argtypes = [mmp, vp, vp, vp, vp, vp]
+    L.moe_quant_i8.argtypes = [C.c_int, C.c_int, C.c_int, C.c_int, vp, vp, vp, vp]
+    L.moe_mm_i8.argtypes = [mmp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.moe_linear_i8_workspace_size.argtypes = [mmp, C.c_int, C.POINTER(sz)]
+    L.moe_linear_i8.argtypes = [mmp, vp, C.c_int, vp, vp, vp, vp, vp, vp, sz, vp]
     L.moe_status_str.argtypes = [C.c_int]
     L.moe_status_str.restype = C.c_char_p
     for n in EXPORTS:
@@ -379,6 +402,220 @@ def moe_encode_e4m3(v: torch.Tensor, codes: Optional[torch.Tensor] = None) -> to
         codes = torch.empty(v.shape, dtype=torch.uint8, device=v.device)
     _check("moe_encode_e4m3", load().moe_encode_e4m3(_ptr(v), v.numel(), _ptr(codes), _stream()))
     return codes
+
+
+# ------------------------------------------------------------------ row-major products
+def _require(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _call(name: str, dev: torch.device, *args) -> None:
+    """A library call on `dev`'s current stream, with that device current."""
+    if dev.index is not None and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            _check(name, getattr(load(), name)(*args, torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        _check(name, getattr(load(), name)(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def _tensor(name: str, t: torch.Tensor, dtypes, shape, dev: torch.device) -> None:
+    """`t` has one of `dtypes`, the `shape` (None: any size) and the device `dev`."""
+    _require(t.dtype in dtypes, f"{name}: dtype {t.dtype} is not one of {', '.join(map(str, dtypes))}")
+    _require(t.dim() == len(shape) and all(want is None or have == want for have, want in zip(t.shape, shape)),
+             f"{name}: shape {tuple(t.shape)}, expected {tuple('any' if v is None else v for v in shape)}")
+    _require(t.device == dev, f"{name} is on {t.device}, the other operands on {dev}")
+
+
+_16BIT = (torch.bfloat16, torch.float16)
+
+
+def _mm_out(name: str, out, shape, dtype, out_dtype, inputs):
+    """The output of a product (checked, or new) and clear_tail: a new one has
+    every row written, a caller's keeps its rows behind the last group."""
+    dev = inputs[0].device
+    if out is None:
+        return torch.empty(shape, dtype=dtype if out_dtype is None else out_dtype, device=dev), 1
+    _require(out_dtype is None or out.dtype == out_dtype, f"{name}: out has dtype {out.dtype}, not {out_dtype}")
+    _tensor("out", out, (dtype, torch.float32) if dtype in _16BIT else tuple(_DT), shape, dev)
+    return out, 0
+
+
+def _grouped_mm(x, w, offsets, out=None, out_dtype=None):
+    _tensor("x", x, _16BIT, (None, None), x.device)
+    _tensor("w", w, (x.dtype,), (None, None, x.shape[1]), x.device)
+    E, N, K = w.shape
+    _tensor("offsets", offsets, (torch.int32,), (E + 1,), x.device)
+    out, clear = _mm_out("moe_grouped_mm", out, (x.shape[0], N), x.dtype, out_dtype, (x, w))
+    c = MoeMmCfg(x.shape[0], N, K, E, 0, _DT[x.dtype], _DT.get(out.dtype, -1), clear)
+    _call("moe_grouped_mm", x.device, C.byref(c), _ptr(x), _ptr(w), _ptr(offsets), _ptr(out))
+    return out
+
+
+def moe_grouped_mm_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
+                         out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """dx [R, K] = dy[r] @ w[e] for the rows r of each group e: moe_grouped_mm's
+    gradient with respect to x.  `out` and `out_dtype` as in moe_grouped_mm."""
+    _tensor("dy", dy, _16BIT, (None, None), dy.device)
+    _tensor("w", w, (dy.dtype,), (None, dy.shape[1], None), dy.device)
+    E, N, K = w.shape
+    _tensor("offsets", offsets, (torch.int32,), (E + 1,), dy.device)
+    out, clear = _mm_out("moe_grouped_mm_dgrad", out, (dy.shape[0], K), dy.dtype, out_dtype, (dy, w))
+    c = MoeMmCfg(dy.shape[0], N, K, E, 0, _DT[dy.dtype], _DT.get(out.dtype, -1), clear)
+    _call("moe_grouped_mm_dgrad", dy.device, C.byref(c), _ptr(dy), _ptr(w), _ptr(offsets), _ptr(out))
+    return out
+
+
+def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
+                         out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """dw [E, N, K] = dy[r]^T x[r] summed over the rows r of each group e (zeros
+    for an empty group): moe_grouped_mm's gradient with respect to w.
+    `out_dtype`: dy's (default) or torch.float32; `out` is fully overwritten."""
+    _tensor("dy", dy, _16BIT, (None, None), dy.device)
+    _tensor("x", x, (dy.dtype,), (dy.shape[0], None), dy.device)
+    _require(offsets.dim() == 1 and offsets.shape[0] >= 2, f"offsets: shape {tuple(offsets.shape)}, expected (E + 1,)")
+    _tensor("offsets", offsets, (torch.int32,), (None,), dy.device)
+    E, (R, N), K = offsets.shape[0] - 1, dy.shape, x.shape[1]
+    out, _ = _mm_out("moe_grouped_mm_wgrad", out, (E, N, K), dy.dtype, out_dtype, (dy, x))
+    c = MoeMmCfg(R, N, K, E, 0, _DT[dy.dtype], _DT.get(out.dtype, -1), 0)
+    _call("moe_grouped_mm_wgrad", dy.device, C.byref(c), _ptr(dy), _ptr(x), _ptr(offsets), _ptr(out))
+    return out
+
+
+class _GroupedMM(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offsets):
+        ctx.save_for_backward(x, w, offsets)
+        return _grouped_mm(x, w, offsets)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, w, offsets = ctx.saved_tensors
+        dy = dy.contiguous()
+        dx = moe_grouped_mm_dgrad(dy, w, offsets) if ctx.needs_input_grad[0] else None
+        dw = moe_grouped_mm_wgrad(dy, x, offsets) if ctx.needs_input_grad[1] else None
+        return dx, dw, None
+
+
+def moe_grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out: Optional[torch.Tensor] = None,
+                   out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """y [R, N] = x[r] @ w[e]^T for the rows r = offsets[e] .. offsets[e + 1] - 1
+    of each group e, w [E, N, K] row-major.
+
+    x and w are both bfloat16 or both float16; offsets is int32 [E + 1] on the
+    same device (moe_permute's).  The result has x's type, or float32 with
+    out_dtype=torch.float32 (the rows moe_combine takes).  Rows behind the last
+    group (r >= offsets[E]) are zeros in a new result; a caller's `out` keeps
+    what it holds there.
+
+    Differentiable with respect to x and w (once; not with `out` or
+    `out_dtype`): the gradients are moe_grouped_mm_dgrad and
+    moe_grouped_mm_wgrad, and rows behind the last group get the gradient 0."""
+    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad):
+        _require(out is None and out_dtype in (None, x.dtype),
+                 "moe_grouped_mm: out and out_dtype cannot be given where a gradient is needed")
+        return _GroupedMM.apply(x, w, offsets)
+    return _grouped_mm(x, w, offsets, out, out_dtype)
+
+
+def moe_quant_i8(x: torch.Tensor, swiglu: bool = False, codes: Optional[torch.Tensor] = None,
+                 scales: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """int8 codes [R, K] and fp32 scales [R] of the rows of x [R, K] (bfloat16 or
+    float16), or of silu(gate) * up with x [R, 2 K] = gate | up where `swiglu`.
+    value = code * scale; a row with an infinity or NaN gets the scale NaN."""
+    _tensor("x", x, _16BIT, (None, None), x.device)
+    R, K = x.shape[0], x.shape[1]
+    if swiglu:
+        _require(K % 2 == 0, f"x: {K} columns do not split into gate and up")
+        K //= 2
+    if codes is None:
+        codes = torch.empty(R, K, dtype=torch.int8, device=x.device)
+    if scales is None:
+        scales = torch.empty(R, dtype=torch.float32, device=x.device)
+    _tensor("codes", codes, (torch.int8,), (R, K), x.device)
+    _tensor("scales", scales, (torch.float32,), (R,), x.device)
+    _call("moe_quant_i8", x.device, R, K, _DT[x.dtype], int(bool(swiglu)), _ptr(x), _ptr(codes), _ptr(scales))
+    return codes, scales
+
+
+def _i8_weights(wq, ws, offsets, dev):
+    """(E, N, K) of int8 weights [E, N, K], or [N, K] (dense: no offsets)."""
+    _require(wq.dim() == (2 if offsets is None else 3),
+             "wq: [N, K] without offsets, [E, N, K] with offsets; got %s" % (tuple(wq.shape),))
+    _tensor("wq", wq, (torch.int8,), (None,) * wq.dim(), dev)
+    _tensor("ws", ws, (torch.float32,), wq.shape[:-1], dev)
+    E, N, K = (1, *wq.shape) if offsets is None else wq.shape
+    if offsets is not None:
+        _tensor("offsets", offsets, (torch.int32,), (E + 1,), dev)
+    return E, N, K
+
+
+def moe_mm_i8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
+              offsets: Optional[torch.Tensor] = None, row_token: Optional[torch.Tensor] = None,
+              out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """y[r] = (xq[t] @ wq[e]^T) * xs[t] * ws[e] with int8 operands, exact integer
+    sums, one scale per row of xq and one per output channel.
+
+    Dense: wq [N, K], ws [N], every row of xq.  Grouped: wq [E, N, K], ws
+    [E, N] and offsets int32 [E + 1]; with row_token int32 [R] (moe_permute's)
+    row r of the result takes row t = row_token[r] of xq, else t = r.
+    The result [R, N] is bfloat16, float16 or float32; rows behind the last
+    group are zeros in a new result and stay as they are in a caller's `out`."""
+    _tensor("xq", xq, (torch.int8,), (None, None), xq.device)
+    T = xq.shape[0]
+    _tensor("xs", xs, (torch.float32,), (T,), xq.device)
+    E, N, K = _i8_weights(wq, ws, offsets, xq.device)
+    _require(K == xq.shape[1], f"wq: {K} inputs, xq has {xq.shape[1]}")
+    R = T
+    if row_token is not None:
+        _tensor("row_token", row_token, (torch.int32,), (None,), xq.device)
+        R = row_token.shape[0]
+    if out is not None:
+        out_dtype = out.dtype
+    _require(out_dtype in _DT, f"out_dtype {out_dtype} is not one of {', '.join(map(str, _DT))}")
+    out, clear = _mm_out("moe_mm_i8", out, (R, N), torch.int8, out_dtype, (xq,))
+    c = MoeMmCfg(R, N, K, E, T, 0, _DT[out.dtype], clear)
+    _call("moe_mm_i8", xq.device, C.byref(c), _ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), _ptr(offsets), _ptr(row_token),
+          _ptr(out))
+    return out
+
+
+def moe_linear_i8_workspace_size(rows: int, K: int) -> int:
+    """Bytes of scratch moe_linear_i8 needs for x of `rows` rows and K inputs of w."""
+    n, c = C.c_size_t(0), MoeMmCfg(rows, 8, K, 1, rows, 0, 0, 0)
+    _check("moe_linear_i8_workspace_size", load().moe_linear_i8_workspace_size(C.byref(c), 0, C.byref(n)))
+    return int(n.value)
+
+
+def moe_linear_i8(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets: Optional[torch.Tensor] = None,
+                  row_token: Optional[torch.Tensor] = None, swiglu: bool = False, out: Optional[torch.Tensor] = None,
+                  out_dtype: Optional[torch.dtype] = None, work: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_mm_i8 of moe_quant_i8(x, swiglu): 16-bit activations (bfloat16 or
+    float16) times int8 weights.  The result has x's type unless out_dtype or
+    `out` says otherwise.  `work`: uint8 scratch of at least
+    moe_linear_i8_workspace_size(x.shape[0], K) bytes, allocated where absent."""
+    _tensor("x", x, _16BIT, (None, None), x.device)
+    T, dev = x.shape[0], x.device
+    E, N, K = _i8_weights(wq, ws, offsets, dev)
+    _require(x.shape[1] == (2 * K if swiglu else K), f"x: {x.shape[1]} columns, wq has {K} inputs")
+    R = T
+    if row_token is not None:
+        _tensor("row_token", row_token, (torch.int32,), (None,), dev)
+        R = row_token.shape[0]
+    if out is not None:
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = x.dtype
+    _require(out_dtype in _DT, f"out_dtype {out_dtype} is not one of {', '.join(map(str, _DT))}")
+    out, clear = _mm_out("moe_linear_i8", out, (R, N), torch.int8, out_dtype, (x,))
+    c = MoeMmCfg(R, N, K, E, T, _DT[x.dtype], _DT[out.dtype], clear)
+    if work is None:
+        work = torch.empty(moe_linear_i8_workspace_size(T, K), dtype=torch.uint8, device=dev)
+    _tensor("work", work, (torch.uint8,), (None,), dev)
+    _call("moe_linear_i8", dev, C.byref(c), _ptr(x), int(bool(swiglu)), _ptr(wq), _ptr(ws), _ptr(offsets),
+          _ptr(row_token), _ptr(out), _ptr(work), work.numel())
+    return out
 
 
 def raw_call(name: str, *args) -> int:

@@ -1,0 +1,44 @@
+// moe_mm.h -- internal interface between the ABI of the row-major products
+// (moe_mm_api.hip) and their kernels (moe_mm.hip, moe_quant_i8.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace moe {
+
+// Operand types of the products and element types of their outputs
+// (MOE_DT_* of the ABI; int8 is internal).
+constexpr int kBf16 = 0, kFp16 = 1, kFp32 = 2, kInt8 = 3;
+
+// The three products over ragged groups e of rows r:
+//   kFwd    y[r][n]  = sum_k x[r][k]  w[e][n][k]   (reduction K)
+//   kDgrad  dx[r][k] = sum_n dy[r][n] w[e][n][k]   (reduction N)
+//   kWgrad  dw[e][n][k] = sum_{r in e} dy[r][n] x[r][k]
+constexpr int kFwd = 0, kDgrad = 1, kWgrad = 2;
+
+struct MmArgs {
+  const void* p;             // x (kFwd) or dy: the operand whose index is the output's row
+  const void* q;             // w, or x (kWgrad): its index is the output's column
+  void* out;
+  const int32_t* offsets;    // [E + 1]; null: one group of R rows
+  const int32_t* row_token;  // int8 only: row of p for each output row, or null
+  const float* ps;           // int8 only: scale per row of p
+  const float* qs;           // int8 only: scale per [E][N]
+  int R, N, K, E, T;
+  int ty;                    // operand type
+  int out_ty;                // output type
+  int clear_tail;            // rows behind the last group: 1 written as zeros, 0 left alone
+};
+
+// Number of workgroups of a launch (64-bit: the ABI refuses more than 2^31).
+long mm_grid(int op, const MmArgs& a);
+hipError_t launch_mm(int op, const MmArgs& a, hipStream_t st);
+
+// Per-token int8 quantisation of rows of `ty` (kBf16 / kFp16): K values per
+// row, or SwiGLU of 2 K (gate first).
+hipError_t launch_quant_i8(const void* x, int ty, int swiglu, int R, int K, int8_t* codes, float* scales,
+                           hipStream_t st);
+
+}  // namespace moe

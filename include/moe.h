@@ -322,6 +322,94 @@ int moe_layer_static(const moe_cfg* cfg, const uint16_t* x, const int32_t* topk_
  * enqueued on `stream` like every other call. */
 int moe_prepack_weights(const moe_cfg* cfg, const moe_weights* canonical, moe_weights* packed, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Products on ROW-MAJOR weights: the expert product in 16 bits with both its
+ * gradients (fine-tuning the experts, or running them before they are
+ * quantised), and the int8 product with one scale per token and one per
+ * output channel (the number format of the FusedDeepMoE chain: int8 tokens
+ * with a per-token scale, int8 weights with a per-channel scale), grouped by
+ * expert or dense.
+ *
+ * Groups: rows offsets[e] .. offsets[e + 1] - 1 belong to group e, with
+ * offsets[0] = 0 and offsets not decreasing (moe_permute's offsets of a cfg
+ * without a shared expert).  Groups may be empty.  Rows from offsets[E] to R
+ * belong to none: a product with clear_tail = 1 writes zeros to them, with
+ * clear_tail = 0 it leaves them as they were.  Offsets are read on the device
+ * and clamped to [0, R]: a wrong array gives wrong results, never an access
+ * outside the tensors.
+ *
+ * moe_mm_cfg (host struct):
+ *   R rows, N outputs and K inputs of a weight matrix, E groups (1 .. 1024),
+ *   T tokens (only with row_token), dtype of the 16-bit operands
+ *   (MOE_DT_BF16 / MOE_DT_FP16), out_dtype (that type or MOE_DT_FP32),
+ *   clear_tail as above.
+ * Limits: N and K multiples of 8 up to 2^20 (int8: K a multiple of 16 up to
+ *   2^16, which keeps every sum inside an int32), MOE_ERR_BAD_SHAPE
+ *   otherwise.  R * K and R * N may pass 2^32.
+ * Sums are kept in fp32 (int8: exactly, in int32) and rounded once to
+ * out_dtype.  Infinities and NaN stay in their row (in wgrad: in their
+ * group). */
+enum { MOE_DT_BF16 = 0, MOE_DT_FP16 = 1, MOE_DT_FP32 = 2 };
+typedef struct moe_mm_cfg {
+  int32_t R, N, K, E, T;
+  int32_t dtype;
+  int32_t out_dtype;
+  int32_t clear_tail;
+} moe_mm_cfg;
+
+/* y[r][n] = sum_k x[r][k] * w[e][n][k] for the rows r of each group e.
+ *   x [R][K], w [E][N][K] of dtype; offsets int32 [E + 1]; y [R][N] of
+ *   out_dtype (distinct from x).  x and y may be NULL for R = 0. */
+int moe_grouped_mm(const moe_mm_cfg* cfg, const void* x, const void* w, const int32_t* offsets, void* y,
+                   void* stream);
+
+/* The gradient with respect to x: dx[r][k] = sum_n dy[r][n] * w[e][n][k].
+ *   dy [R][N], w [E][N][K] of dtype; dx [R][K] of out_dtype.  clear_tail = 1
+ *   gives rows of no group the gradient 0. */
+int moe_grouped_mm_dgrad(const moe_mm_cfg* cfg, const void* dy, const void* w, const int32_t* offsets, void* dx,
+                         void* stream);
+
+/* The gradient with respect to w: dw[e][n][k] = sum over the rows r of group
+ * e of dy[r][n] * x[r][k]; zeros for an empty group.
+ *   dy [R][N], x [R][K] of dtype; dw [E][N][K] of out_dtype, fully
+ *   overwritten.  The sum's order is fixed: equal inputs give equal bits. */
+int moe_grouped_mm_wgrad(const moe_mm_cfg* cfg, const void* dy, const void* x, const int32_t* offsets, void* dw,
+                         void* stream);
+
+/* Per-token int8 quantisation (the FusedDeepMoE analysis's QuantToken): for
+ * each row v of K values, a = max |v|, m = 127 / max(a, 2^-64) (fp32,
+ * correctly rounded), code = v * m rounded to nearest even, scale = 1 / m.
+ * A row that holds an infinity or NaN gets codes 0 and the scale NaN, so that
+ * every result made from it is NaN.
+ *   x      [R][K] of dtype; swiglu = 1: [R][2 K], v = silu(x[:, :K]) *
+ *          x[:, K:] in fp32 (the layer's SwiGLU)
+ *   codes  int8 [R][K]; scales fp32 [R]
+ * K a multiple of 16 up to 2^20 (MOE_ERR_BAD_SHAPE otherwise). */
+int moe_quant_i8(int R, int K, int dtype, int swiglu, const void* x, int8_t* codes, float* scales, void* stream);
+
+/* The int8 product: y[r][n] = (sum_k xq[t][k] * wq[e][n][k]) * xs[t] *
+ * ws[e][n], t = row_token[r], or r where row_token is NULL.
+ *   xq int8 and xs fp32: [T][K] and [T] with row_token, else [R][K] and [R]
+ *   wq int8 [E][N][K]; ws fp32 [E][N]
+ *   offsets    int32 [E + 1], or NULL for one dense matrix (E = 1, every row)
+ *   row_token  int32 [R] as moe_permute's, or NULL; a row whose index lies
+ *              outside [0, T) counts as a row of zeros.  T * K < 2^31
+ *              (MOE_ERR_BAD_SHAPE otherwise)
+ *   y          [R][N] of out_dtype: MOE_DT_BF16, MOE_DT_FP16 or MOE_DT_FP32
+ *              (the rows moe_combine takes)
+ * cfg->dtype is not used. */
+int moe_mm_i8(const moe_mm_cfg* cfg, const int8_t* xq, const float* xs, const int8_t* wq, const float* ws,
+              const int32_t* offsets, const int32_t* row_token, void* y, void* stream);
+
+/* moe_quant_i8 of x and moe_mm_i8 in one call.
+ *   x  of dtype, [T][K] with row_token, else [R][K] (swiglu = 1: 2 K wide)
+ *   work: device scratch of moe_linear_i8_workspace_size(cfg, row_token !=
+ *   NULL) bytes (contents on entry ignored; NULL when that size is 0). */
+int moe_linear_i8_workspace_size(const moe_mm_cfg* cfg, int gathered, size_t* bytes);
+int moe_linear_i8(const moe_mm_cfg* cfg, const void* x, int swiglu, const int8_t* wq, const float* ws,
+                  const int32_t* offsets, const int32_t* row_token, void* y, void* work, size_t work_bytes,
+                  void* stream);
+
 /* Diagnostic: read `bytes` (a multiple of 16) of device memory at `buf`
  * once -- a plain HBM read stream, the achievable-bandwidth reference for
  * the weight-streaming GEMMs.  Four workgroups of four waves per CU; each
