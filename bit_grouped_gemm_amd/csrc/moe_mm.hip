@@ -317,18 +317,24 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
       for (int i = 0; i < MF; ++i)
 #pragma unroll
         for (int j = 0; j < NF; ++j) acc[i][j] = mma<TY>(qf[j], pf[i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
+  // a stage's barrier: its loads have arrived, the other stage is no longer read
   if (steps > 0) issue(p0, q0);
-  for (int s = 0; s < steps; s += 2) {
-    stage_barrier();  // stage 0 has arrived, stage 1 is no longer read
-    if (s + 1 < steps) issue(p1, q1);
+  int s = 0;
+  for (; s + 1 < steps; s += 2) {
+    stage_barrier();
+    issue(p1, q1);
     multiply(p0, q0);
-    if (s + 1 >= steps) break;
     stage_barrier();
     if (s + 2 < steps) issue(p0, q0);
     multiply(p1, q1);
+  }
+  if (s < steps) {
+    stage_barrier();
+    multiply(p0, q0);
   }
 
   // lane l holds column 4 (l / 16) + 0..3 and row l % 16 of each fragment
