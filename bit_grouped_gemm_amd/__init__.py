@@ -405,65 +405,87 @@ def moe_encode_e4m3(v: torch.Tensor, codes: Optional[torch.Tensor] = None) -> to
 
 
 # ------------------------------------------------------------------ row-major products
-def _require(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
-
-
-def _call(name: str, dev: torch.device, *args) -> None:
-    """A library call on `dev`'s current stream, with that device current."""
-    if dev.index is not None and dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            _check(name, getattr(load(), name)(*args, torch.cuda.current_stream(dev).cuda_stream))
-    else:
-        _check(name, getattr(load(), name)(*args, torch.cuda.current_stream(dev).cuda_stream))
-
-
-def _tensor(name: str, t: torch.Tensor, dtypes, shape, dev: torch.device) -> None:
-    """`t` has one of `dtypes`, the `shape` (None: any size) and the device `dev`."""
-    _require(t.dtype in dtypes, f"{name}: dtype {t.dtype} is not one of {', '.join(map(str, dtypes))}")
-    _require(t.dim() == len(shape) and all(want is None or have == want for have, want in zip(t.shape, shape)),
-             f"{name}: shape {tuple(t.shape)}, expected {tuple('any' if v is None else v for v in shape)}")
-    _require(t.device == dev, f"{name} is on {t.device}, the other operands on {dev}")
-
-
 _16BIT = (torch.bfloat16, torch.float16)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda index: torch.cuda.current_stream(index).cuda_stream
 
 
-def _mm_out(name: str, out, shape, dtype, out_dtype, inputs):
-    """The output of a product (checked, or new) and clear_tail: a new one has
-    every row written, a caller's keeps its rows behind the last group."""
-    dev = inputs[0].device
-    if out is None:
-        return torch.empty(shape, dtype=dtype if out_dtype is None else out_dtype, device=dev), 1
-    _require(out_dtype is None or out.dtype == out_dtype, f"{name}: out has dtype {out.dtype}, not {out_dtype}")
-    _tensor("out", out, (dtype, torch.float32) if dtype in _16BIT else tuple(_DT), shape, dev)
-    return out, 0
+def _call(name: str, index: int, *args) -> None:
+    """A library call on the current stream of device `index`, with that device current."""
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            rc = getattr(_lib or load(), name)(*args, _raw_stream(index))
+    else:
+        rc = getattr(_lib or load(), name)(*args, _raw_stream(index))
+    if rc:
+        raise MoeError(name, rc)
+
+
+def _addr(name: str, t: torch.Tensor, dtypes, shape, dev: torch.device):
+    """The address of a contiguous GPU tensor of one of `dtypes`, of `shape`
+    (None: any size) and on `dev`; None where it is empty.  A message is only
+    put together for a tensor that is none."""
+    if t.dtype in dtypes and t.shape == shape and t.device == dev and t.is_cuda and t.is_contiguous():
+        return t.data_ptr() or None
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype} is not one of {', '.join(map(str, dtypes))}")
+    if t.dim() != len(shape) or any(w is not None and h != w for h, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple('any' if v is None else v for v in shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the other operands on {dev}")
+    return _ptr(t)
+
+
+def _new_or_checked(out, shape, dtype, allowed, dev):
+    """The output tensor and clear_tail: a new one has every row written, a
+    caller's keeps its rows behind the last group."""
+    if out is not None:
+        return out, 0
+    if dtype not in allowed:
+        raise ValueError(f"out_dtype {dtype} is not one of {', '.join(map(str, allowed))}")
+    return torch.empty(shape, dtype=dtype, device=dev), 1
+
+
+def _matrices(w: torch.Tensor):
+    if w.dim() != 3:
+        raise ValueError(f"w: shape {tuple(w.shape)}, expected (E, N, K)")
+    return w.shape
+
+
+def _rows_of(name: str, t: torch.Tensor) -> torch.Size:
+    if t.dim() != 2:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected two dimensions")
+    return t.shape
+
+
+def _grouped(name, rows, p, w, offsets, width, other, out, out_dtype):
+    """y from x, or dx from dy: `p` [R, width] times the matrices w [E, N, K]."""
+    R, dt, dev = _rows_of(rows, p)[0], p.dtype, p.device
+    E, N, K = w.shape
+    allowed = (dt, torch.float32)
+    pp = _addr(rows, p, _16BIT, (R, width), dev)
+    pw = _addr("w", w, (dt,), (E, N, K), dev)
+    po = _addr("offsets", offsets, (torch.int32,), (E + 1,), dev)
+    if out is not None and out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
+    out, clear = _new_or_checked(out, (R, other), out_dtype or dt, allowed, dev)
+    py = _addr("out", out, allowed, (R, other), dev)
+    c = MoeMmCfg(R, N, K, E, 0, _DT[dt], _DT[out.dtype], clear)
+    _call(name, dev.index, C.byref(c), pp, pw, po, py)
+    return out
 
 
 def _grouped_mm(x, w, offsets, out=None, out_dtype=None):
-    _tensor("x", x, _16BIT, (None, None), x.device)
-    _tensor("w", w, (x.dtype,), (None, None, x.shape[1]), x.device)
-    E, N, K = w.shape
-    _tensor("offsets", offsets, (torch.int32,), (E + 1,), x.device)
-    out, clear = _mm_out("moe_grouped_mm", out, (x.shape[0], N), x.dtype, out_dtype, (x, w))
-    c = MoeMmCfg(x.shape[0], N, K, E, 0, _DT[x.dtype], _DT.get(out.dtype, -1), clear)
-    _call("moe_grouped_mm", x.device, C.byref(c), _ptr(x), _ptr(w), _ptr(offsets), _ptr(out))
-    return out
+    _, N, K = _matrices(w)
+    return _grouped("moe_grouped_mm", "x", x, w, offsets, K, N, out, out_dtype)
 
 
 def moe_grouped_mm_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
                          out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """dx [R, K] = dy[r] @ w[e] for the rows r of each group e: moe_grouped_mm's
     gradient with respect to x.  `out` and `out_dtype` as in moe_grouped_mm."""
-    _tensor("dy", dy, _16BIT, (None, None), dy.device)
-    _tensor("w", w, (dy.dtype,), (None, dy.shape[1], None), dy.device)
-    E, N, K = w.shape
-    _tensor("offsets", offsets, (torch.int32,), (E + 1,), dy.device)
-    out, clear = _mm_out("moe_grouped_mm_dgrad", out, (dy.shape[0], K), dy.dtype, out_dtype, (dy, w))
-    c = MoeMmCfg(dy.shape[0], N, K, E, 0, _DT[dy.dtype], _DT.get(out.dtype, -1), clear)
-    _call("moe_grouped_mm_dgrad", dy.device, C.byref(c), _ptr(dy), _ptr(w), _ptr(offsets), _ptr(out))
-    return out
+    _, N, K = _matrices(w)
+    return _grouped("moe_grouped_mm_dgrad", "dy", dy, w, offsets, N, K, out, out_dtype)
 
 
 def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
@@ -471,14 +493,20 @@ def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     """dw [E, N, K] = dy[r]^T x[r] summed over the rows r of each group e (zeros
     for an empty group): moe_grouped_mm's gradient with respect to w.
     `out_dtype`: dy's (default) or torch.float32; `out` is fully overwritten."""
-    _tensor("dy", dy, _16BIT, (None, None), dy.device)
-    _tensor("x", x, (dy.dtype,), (dy.shape[0], None), dy.device)
-    _require(offsets.dim() == 1 and offsets.shape[0] >= 2, f"offsets: shape {tuple(offsets.shape)}, expected (E + 1,)")
-    _tensor("offsets", offsets, (torch.int32,), (None,), dy.device)
-    E, (R, N), K = offsets.shape[0] - 1, dy.shape, x.shape[1]
-    out, _ = _mm_out("moe_grouped_mm_wgrad", out, (E, N, K), dy.dtype, out_dtype, (dy, x))
-    c = MoeMmCfg(R, N, K, E, 0, _DT[dy.dtype], _DT.get(out.dtype, -1), 0)
-    _call("moe_grouped_mm_wgrad", dy.device, C.byref(c), _ptr(dy), _ptr(x), _ptr(offsets), _ptr(out))
+    (R, N), K, dt, dev = _rows_of("dy", dy), _rows_of("x", x)[1], dy.dtype, dy.device
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError(f"offsets: shape {tuple(offsets.shape)}, expected (E + 1,)")
+    E = offsets.shape[0] - 1
+    allowed = (dt, torch.float32)
+    pd = _addr("dy", dy, _16BIT, (R, N), dev)
+    px = _addr("x", x, (dt,), (R, K), dev)
+    po = _addr("offsets", offsets, (torch.int32,), (E + 1,), dev)
+    if out is not None and out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
+    out, _ = _new_or_checked(out, (E, N, K), out_dtype or dt, allowed, dev)
+    pw = _addr("out", out, allowed, (E, N, K), dev)
+    c = MoeMmCfg(R, N, K, E, 0, _DT[dt], _DT[out.dtype], 0)
+    _call("moe_grouped_mm_wgrad", dev.index, C.byref(c), pd, px, po, pw)
     return out
 
 
@@ -512,9 +540,9 @@ def moe_grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out:
     Differentiable with respect to x and w (once; not with `out` or
     `out_dtype`): the gradients are moe_grouped_mm_dgrad and
     moe_grouped_mm_wgrad, and rows behind the last group get the gradient 0."""
-    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad):
-        _require(out is None and out_dtype in (None, x.dtype),
-                 "moe_grouped_mm: out and out_dtype cannot be given where a gradient is needed")
+    if (x.requires_grad or w.requires_grad) and torch.is_grad_enabled():
+        if out is not None or out_dtype not in (None, x.dtype):
+            raise ValueError("moe_grouped_mm: out and out_dtype cannot be given where a gradient is needed")
         return _GroupedMM.apply(x, w, offsets)
     return _grouped_mm(x, w, offsets, out, out_dtype)
 
@@ -524,60 +552,64 @@ def moe_quant_i8(x: torch.Tensor, swiglu: bool = False, codes: Optional[torch.Te
     """int8 codes [R, K] and fp32 scales [R] of the rows of x [R, K] (bfloat16 or
     float16), or of silu(gate) * up with x [R, 2 K] = gate | up where `swiglu`.
     value = code * scale; a row with an infinity or NaN gets the scale NaN."""
-    _tensor("x", x, _16BIT, (None, None), x.device)
-    R, K = x.shape[0], x.shape[1]
-    if swiglu:
-        _require(K % 2 == 0, f"x: {K} columns do not split into gate and up")
-        K //= 2
+    (R, width), dev = _rows_of("x", x), x.device
+    if swiglu and width % 2:
+        raise ValueError(f"x: {width} columns do not split into gate and up")
+    K = width // 2 if swiglu else width
+    px = _addr("x", x, _16BIT, (R, width), dev)
     if codes is None:
-        codes = torch.empty(R, K, dtype=torch.int8, device=x.device)
+        codes = torch.empty(R, K, dtype=torch.int8, device=dev)
     if scales is None:
-        scales = torch.empty(R, dtype=torch.float32, device=x.device)
-    _tensor("codes", codes, (torch.int8,), (R, K), x.device)
-    _tensor("scales", scales, (torch.float32,), (R,), x.device)
-    _call("moe_quant_i8", x.device, R, K, _DT[x.dtype], int(bool(swiglu)), _ptr(x), _ptr(codes), _ptr(scales))
+        scales = torch.empty(R, dtype=torch.float32, device=dev)
+    pq = _addr("codes", codes, (torch.int8,), (R, K), dev)
+    ps = _addr("scales", scales, (torch.float32,), (R,), dev)
+    _call("moe_quant_i8", dev.index, R, K, _DT[x.dtype], int(bool(swiglu)), px, pq, ps)
     return codes, scales
 
 
 def _i8_weights(wq, ws, offsets, dev):
-    """(E, N, K) of int8 weights [E, N, K], or [N, K] (dense: no offsets)."""
-    _require(wq.dim() == (2 if offsets is None else 3),
-             "wq: [N, K] without offsets, [E, N, K] with offsets; got %s" % (tuple(wq.shape),))
-    _tensor("wq", wq, (torch.int8,), (None,) * wq.dim(), dev)
-    _tensor("ws", ws, (torch.float32,), wq.shape[:-1], dev)
+    """E, N, K and the addresses of int8 weights [E, N, K], or [N, K] (dense: no
+    offsets), of their scales and of the offsets."""
+    if wq.dim() != (2 if offsets is None else 3):
+        raise ValueError(f"wq: [N, K] without offsets, [E, N, K] with offsets; got {tuple(wq.shape)}")
     E, N, K = (1, *wq.shape) if offsets is None else wq.shape
-    if offsets is not None:
-        _tensor("offsets", offsets, (torch.int32,), (E + 1,), dev)
-    return E, N, K
+    pw = _addr("wq", wq, (torch.int8,), wq.shape, dev)
+    ps = _addr("ws", ws, (torch.float32,), wq.shape[:-1], dev)
+    po = None if offsets is None else _addr("offsets", offsets, (torch.int32,), (E + 1,), dev)
+    return E, N, K, pw, ps, po
+
+
+def _row_token(row_token, T, dev):
+    if row_token is None:
+        return T, None
+    if row_token.dim() != 1:
+        raise ValueError(f"row_token: shape {tuple(row_token.shape)}, expected one dimension")
+    return row_token.shape[0], _addr("row_token", row_token, (torch.int32,), row_token.shape, dev)
 
 
 def moe_mm_i8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
               offsets: Optional[torch.Tensor] = None, row_token: Optional[torch.Tensor] = None,
-              out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+              out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """y[r] = (xq[t] @ wq[e]^T) * xs[t] * ws[e] with int8 operands, exact integer
     sums, one scale per row of xq and one per output channel.
 
     Dense: wq [N, K], ws [N], every row of xq.  Grouped: wq [E, N, K], ws
     [E, N] and offsets int32 [E + 1]; with row_token int32 [R] (moe_permute's)
     row r of the result takes row t = row_token[r] of xq, else t = r.
-    The result [R, N] is bfloat16, float16 or float32; rows behind the last
-    group are zeros in a new result and stay as they are in a caller's `out`."""
-    _tensor("xq", xq, (torch.int8,), (None, None), xq.device)
-    T = xq.shape[0]
-    _tensor("xs", xs, (torch.float32,), (T,), xq.device)
-    E, N, K = _i8_weights(wq, ws, offsets, xq.device)
-    _require(K == xq.shape[1], f"wq: {K} inputs, xq has {xq.shape[1]}")
-    R = T
-    if row_token is not None:
-        _tensor("row_token", row_token, (torch.int32,), (None,), xq.device)
-        R = row_token.shape[0]
-    if out is not None:
-        out_dtype = out.dtype
-    _require(out_dtype in _DT, f"out_dtype {out_dtype} is not one of {', '.join(map(str, _DT))}")
-    out, clear = _mm_out("moe_mm_i8", out, (R, N), torch.int8, out_dtype, (xq,))
+    The result [R, N] is bfloat16 (default), float16 or float32; rows behind
+    the last group are zeros in a new result and stay as they are in a
+    caller's `out`."""
+    (T, width), dev = _rows_of("xq", xq), xq.device
+    E, N, K, pw, pws, po = _i8_weights(wq, ws, offsets, dev)
+    pq = _addr("xq", xq, (torch.int8,), (T, K), dev)
+    ps = _addr("xs", xs, (torch.float32,), (T,), dev)
+    R, pt = _row_token(row_token, T, dev)
+    if out is not None and out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
+    out, clear = _new_or_checked(out, (R, N), out_dtype or torch.bfloat16, tuple(_DT), dev)
+    py = _addr("out", out, tuple(_DT), (R, N), dev)
     c = MoeMmCfg(R, N, K, E, T, 0, _DT[out.dtype], clear)
-    _call("moe_mm_i8", xq.device, C.byref(c), _ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), _ptr(offsets), _ptr(row_token),
-          _ptr(out))
+    _call("moe_mm_i8", dev.index, C.byref(c), pq, ps, pw, pws, po, pt, py)
     return out
 
 
@@ -595,26 +627,19 @@ def moe_linear_i8(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets: 
     float16) times int8 weights.  The result has x's type unless out_dtype or
     `out` says otherwise.  `work`: uint8 scratch of at least
     moe_linear_i8_workspace_size(x.shape[0], K) bytes, allocated where absent."""
-    _tensor("x", x, _16BIT, (None, None), x.device)
-    T, dev = x.shape[0], x.device
-    E, N, K = _i8_weights(wq, ws, offsets, dev)
-    _require(x.shape[1] == (2 * K if swiglu else K), f"x: {x.shape[1]} columns, wq has {K} inputs")
-    R = T
-    if row_token is not None:
-        _tensor("row_token", row_token, (torch.int32,), (None,), dev)
-        R = row_token.shape[0]
-    if out is not None:
-        out_dtype = out.dtype
-    elif out_dtype is None:
-        out_dtype = x.dtype
-    _require(out_dtype in _DT, f"out_dtype {out_dtype} is not one of {', '.join(map(str, _DT))}")
-    out, clear = _mm_out("moe_linear_i8", out, (R, N), torch.int8, out_dtype, (x,))
+    (T, _), dev = _rows_of("x", x), x.device
+    E, N, K, pw, pws, po = _i8_weights(wq, ws, offsets, dev)
+    px = _addr("x", x, _16BIT, (T, 2 * K if swiglu else K), dev)
+    R, pt = _row_token(row_token, T, dev)
+    if out is not None and out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
+    out, clear = _new_or_checked(out, (R, N), out_dtype or x.dtype, tuple(_DT), dev)
+    py = _addr("out", out, tuple(_DT), (R, N), dev)
     c = MoeMmCfg(R, N, K, E, T, _DT[x.dtype], _DT[out.dtype], clear)
     if work is None:
         work = torch.empty(moe_linear_i8_workspace_size(T, K), dtype=torch.uint8, device=dev)
-    _tensor("work", work, (torch.uint8,), (None,), dev)
-    _call("moe_linear_i8", dev, C.byref(c), _ptr(x), int(bool(swiglu)), _ptr(wq), _ptr(ws), _ptr(offsets),
-          _ptr(row_token), _ptr(out), _ptr(work), work.numel())
+    pk = _addr("work", work, (torch.uint8,), work.shape, dev)
+    _call("moe_linear_i8", dev.index, C.byref(c), px, int(bool(swiglu)), pw, pws, po, pt, py, pk, work.numel())
     return out
 
 
