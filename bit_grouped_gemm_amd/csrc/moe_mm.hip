@@ -18,6 +18,8 @@
 // Rows, columns and K steps past an operand's end read zeros through the
 // buffer descriptor's bounds check, which ends at the group's last row, so a
 // NaN of another group never meets this one's zeros.
+#include <cmath>
+
 #include "moe_device.h"
 #include "moe_mm.h"
 
@@ -30,15 +32,24 @@ typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 512;
 constexpr int kBN = 256;     // output columns of a tile
+constexpr double kCUs = 256;
 constexpr int kStepRows = 64;  // k rows of a T stage
 constexpr uint32_t kOutside = 0x80000000u;  // a byte offset no descriptor reaches
-
-#define LDS_PTR(p) ((__attribute__((address_space(3))) void*)(p))
 
 template <int N>
 __device__ __forceinline__ void wait_vm() {
   static_assert(N >= 0 && N < 64, "vmcnt range");
   __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+}
+
+// Direct-to-LDS load of 16 bytes per lane: lane l's land at lds + 16 l (lds
+// wave-uniform).  `off` counts from `base`; from `span` on it reads zeros.
+// STREAM: read once, so not kept in the caches (non-temporal).
+template <bool STREAM>
+__device__ __forceinline__ void dma16(const uint8_t* base, uint32_t span, uint32_t off, uint8_t* lds) {
+  auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, span, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, 0, 0,
+                                           STREAM ? 2 : 0);
 }
 
 // Barrier after this wave's LDS accesses and loads have completed; nothing is
@@ -77,50 +88,49 @@ __device__ __forceinline__ int2 group_rows(const int32_t* offsets, int e, int E,
 __device__ __forceinline__ bool find_tile(const MmArgs& a, int BM, int ncol, int id, Place& pl, int& col) {
   const int lane = threadIdx.x & 63;
   const int G = a.E + (a.clear_tail ? 1 : 0);
-  int total = 0;
-  for (int e0 = 0; e0 < G; e0 += 64) {
-    int n = 0;
-    if (e0 + lane < G) {
-      const int2 r = group_rows(a.offsets, e0 + lane, a.E, a.R);
-      n = (r.y - r.x + BM - 1) / BM;
-    }
-    for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d, 64);
-    total += n;
-  }
-  total = __builtin_amdgcn_readfirstlane(total);
-  const long tiles = long(total) * ncol;
-  const long per = (tiles + 7) / 8;
-  const long t = (id & 7) * per + (id >> 3);
-  if ((id >> 3) >= per || t >= tiles) return false;
-  const long block = t / (4L * ncol);
-  const int in = int(t - block * 4 * ncol);
-  const int wide = int(min(4L, total - block * 4));  // row tiles of this block of columns
-  col = in / wide;
-  const int want = int(block * 4) + in % wide;
-  int before = 0;
-  for (int e0 = 0; e0 < G; e0 += 64) {
-    int n = 0;
-    int2 r = make_int2(0, 0);
+  // inclusive scan of 64 groups' tile counts, from group e0 on
+  int2 r;
+  int n, incl;
+  auto scan = [&](int e0) __attribute__((always_inline)) {
+    n = 0;
+    r = make_int2(0, 0);
     if (e0 + lane < G) {
       r = group_rows(a.offsets, e0 + lane, a.E, a.R);
       n = (r.y - r.x + BM - 1) / BM;
     }
-    int incl = n;
+    incl = n;
+#pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int v = __shfl_up(incl, d, 64);
       if (lane >= d) incl += v;
     }
+  };
+  int total = 0;
+  for (int e0 = 0; e0 < G; e0 += 64) {
+    scan(e0);
+    total += __builtin_amdgcn_readlane(incl, 63);
+  }
+  // the ABI keeps the tiles of a launch under 2^31
+  const uint32_t tiles = uint32_t(total) * uint32_t(ncol), per = (tiles + 7) / 8;
+  const uint32_t t = (id & 7) * per + (id >> 3);
+  if (uint32_t(id >> 3) >= per || t >= tiles) return false;
+  const uint32_t block = t / (4u * ncol), in = t - block * 4u * ncol;
+  const uint32_t wide = min(4u, uint32_t(total) - block * 4u);  // row tiles of this block of columns
+  col = int(in / wide);
+  const int want = int(block * 4u + in % wide);
+  int before = 0;
+  for (int e0 = 0; e0 < G; e0 += 64) {
+    if (G > 64) scan(e0);  // else as it stands
     const uint64_t past = __ballot(before + incl > want);
     if (past) {
       const int l = __ffsll((unsigned long long)past) - 1;
-      const int first = before + __shfl(incl - n, l, 64);
-      const int x = __shfl(r.x, l, 64), y = __shfl(r.y, l, 64);
-      pl.e = __builtin_amdgcn_readfirstlane(e0 + l);
-      pl.row0 = __builtin_amdgcn_readfirstlane(x + (want - first) * BM);
-      pl.rows = min(BM, __builtin_amdgcn_readfirstlane(y) - pl.row0);
+      const int first = before + __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(n, l);
+      pl.e = e0 + l;
+      pl.row0 = __builtin_amdgcn_readlane(r.x, l) + (want - first) * BM;
+      pl.rows = min(BM, __builtin_amdgcn_readlane(r.y, l) - pl.row0);
       return true;
     }
-    before += __shfl(incl, 63, 64);
+    before += __builtin_amdgcn_readlane(incl, 63);
   }
   return false;
 }
@@ -149,6 +159,21 @@ __device__ __forceinline__ void store4(void* out, long at, const v4f& v, int ty)
   } else {
     typedef __bf16 b4 __attribute__((ext_vector_type(4)));
     *reinterpret_cast<b4*>(static_cast<__bf16*>(out) + at) = __builtin_convertvector(v, b4);
+  }
+}
+
+// The result of a sum: itself, or for int8 (sum * token's scale) * channel's
+// scales (in fp32).  Rows behind the last group, and rows that name no token,
+// have sums of zero and no scale.
+template <int TY>
+__device__ __forceinline__ v4f scaled(const MmArgs& a, int e, int row, int c, const typename Acc<TY>::type& sum) {
+  if constexpr (TY == kInt8) {
+    if (e == a.E) return v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const int t = a.row_token ? a.row_token[row] : row;
+    if (a.row_token && (t < 0 || t >= a.T)) return v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    return __builtin_convertvector(sum, v4f) * a.ps[t] * *reinterpret_cast<const v4f*>(a.qs + long(e) * a.N + c);
+  } else {
+    return sum;
   }
 }
 
@@ -197,12 +222,9 @@ struct Stream {
   // (a multiple of 16; chunks past them read as zeros).
   __device__ __forceinline__ void issue(uint8_t* stage, int w, int kleft) const {
     const uint32_t n = uint32_t(left < 0 ? 0L : left > 0x7FFFFFFFL ? 0x7FFFFFFFL : left);
-    auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, n, 0x00020000);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const uint32_t o = TR || chunk < kleft ? off[i] : kOutside;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(stage + (w * kLoads + i) * 1024), 16, o, 0, 0, 0);
-    }
+    for (int i = 0; i < kLoads; ++i)
+      dma16<false>(base, n, TR || chunk < kleft ? off[i] : kOutside, stage + (w * kLoads + i) * 1024);
   }
   __device__ __forceinline__ void advance() {
     base += step;
@@ -344,69 +366,231 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
   for (int i = 0; i < MF; ++i) {
     const int r = wm * (BM / 2) + i * 16 + m;
     if (r >= pl.rows) continue;
-    float sr = 0.0f;
-    if constexpr (TY == kInt8) {
-      if (pl.e < a.E) {
-        const int t = a.row_token ? a.row_token[pl.row0 + r] : pl.row0 + r;
-        if (!a.row_token || (t >= 0 && t < a.T)) sr = a.ps[t];
-      }
-    }
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
       const int c = ct * kBN + wn * 64 + j * 16 + 4 * g;
       if (c >= cols) continue;
-      v4f v;
-      if constexpr (TY == kInt8) {
-        v = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        if (pl.e < a.E) {
-          const v4f sc = *reinterpret_cast<const v4f*>(a.qs + long(pl.e) * a.N + c);
-          v = __builtin_convertvector(acc[i][j], v4f) * sr * sc;
-        }
-      } else {
-        v = acc[i][j];
-      }
-      store4(a.out, (out_row0 + r) * cols + c, v, a.out_ty);
+      store4(a.out, (out_row0 + r) * cols + c, scaled<TY>(a, pl.e, pl.row0 + r, c, acc[i][j]), a.out_ty);
     }
   }
 }
 
-int row_tile(int op, const MmArgs& a) {
-  if (op == kWgrad) return 256;
-  const long groups = a.E < a.R ? a.E : (a.R > 0 ? a.R : 1);
-  const double avg = double(a.R) / double(groups);
-  return avg >= 384 ? 256 : avg >= 96 ? 128 : 64;
+// The forward product where there are too few tiles for the chip (decoding, and
+// dense products of up to a few hundred rows).  A workgroup makes 16 NC columns
+// by 16 NT rows; each of its four waves takes a quarter of the K steps through
+// a ring of S stages of its own, so nothing waits for another wave until the
+// sums are added up, in the order of the waves, through LDS.  Bound by the
+// weights' bytes and their latency: S - 1 steps of 2 KB per 16 columns are in
+// flight per wave, on every CU.
+constexpr int kFewWaves = 4;
+
+template <int TY, int NC, int NT, int S>
+__global__ __launch_bounds__(kFewWaves * 64) void k_mm_few(MmArgs a) {
+  constexpr int kEl = TY == kInt8 ? 1 : 2;
+  constexpr int L = 2 * (NC + NT);       // loads of a wave per step
+  constexpr int kStage = L * 1024;       // bytes of a wave's stage
+  typedef typename Acc<TY>::type acc_t;
+  // one array per stage: see k_mm
+  __shared__ __align__(1024) uint8_t st0[kFewWaves * kStage];
+  __shared__ __align__(1024) uint8_t st1[kFewWaves * kStage];
+  __shared__ __align__(1024) uint8_t st2[S >= 3 ? kFewWaves * kStage : 16];
+  __shared__ __align__(1024) uint8_t st3[S >= 4 ? kFewWaves * kStage : 16];
+  static_assert(S >= 2 && S <= 4 && (S - 1) * L < 64, "ring");
+  static_assert(NC * NT * 1024 <= kStage, "a wave's sums fit a stage");
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = lane & 15, g = lane >> 4;
+  const int ncol = (a.N + 16 * NC - 1) / (16 * NC);
+  Place pl;
+  int ct;
+  if (!find_tile(a, 16 * NT, ncol, blockIdx.x, pl, ct)) return;
+  const int ld = a.K * kEl;  // bytes per row of both operands
+  const int n0 = ct * 16 * NC;
+  const int steps = pl.e == a.E ? 0 : (ld + 127) / 128;
+  const int each = (steps + kFewWaves - 1) / kFewWaves;
+  const int s0 = w * each, mine = max(0, min(steps - s0, each));
+
+  const uint8_t* wq = static_cast<const uint8_t*>(a.q) + (long(pl.e) * a.N + n0) * ld;
+  const uint32_t wspan = uint32_t(min(16 * NC, a.N - n0)) * uint32_t(ld);
+  const uint8_t* pq = static_cast<const uint8_t*>(a.p) + (a.row_token ? 0 : long(pl.row0) * ld);
+  const uint32_t pspan = uint32_t(a.row_token ? a.T : pl.rows) * uint32_t(ld);
+  // load i of a step covers rows 8 i .. 8 i + 7 of its operand; lane l has
+  // row l / 8 and the 16-byte chunk that belongs in its slot l % 8
+  const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+  uint32_t ow[2 * NC], op[2 * NT];
+#pragma unroll
+  for (int i = 0; i < 2 * NC; ++i) ow[i] = uint32_t(8 * i + (lane >> 3)) * uint32_t(ld) + chunk;
+#pragma unroll
+  for (int i = 0; i < 2 * NT; ++i) {
+    const int r = 8 * i + (lane >> 3);
+    int t = r;
+    if (a.row_token) {
+      t = r < pl.rows ? a.row_token[pl.row0 + r] : -1;
+      if (t >= a.T) t = -1;
+    }
+    op[i] = r < pl.rows && t >= 0 ? uint32_t(t) * uint32_t(ld) + chunk : kOutside;
+  }
+
+  acc_t acc[NC][NT];
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = acc_t{0, 0, 0, 0};
+
+  // step k of this wave; past its last one the loads read nothing, so that
+  // every step has L loads for the waits to count
+  auto issue = [&](uint8_t* stage, int k) __attribute__((always_inline)) {
+    const int at = (s0 + k) * 128;
+    const bool in = k < mine && chunk < ld - at;
+    uint8_t* to = stage + w * kStage;
+#pragma unroll
+    for (int i = 0; i < 2 * NC; ++i) dma16<true>(wq, wspan, in ? ow[i] + at : kOutside, to + i * 1024);
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i)
+      dma16<false>(pq, pspan, in && op[i] != kOutside ? op[i] + at : kOutside, to + (2 * NC + i) * 1024);
+  };
+  auto multiply = [&](const uint8_t* stage) __attribute__((always_inline)) {
+    wait_vm<(S - 1) * L>();
+    __builtin_amdgcn_sched_barrier(0);
+    const uint8_t* sq = stage + w * kStage;
+    const uint8_t* sp = sq + 2 * NC * 1024;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      v4i qf[NC], pf[NT];
+#pragma unroll
+      for (int i = 0; i < NC; ++i) qf[i] = read_frag<false, 16 * NC>(sq, i, kk, lane);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) pf[j] = read_frag<false, 16 * NT>(sp, j, kk, lane);
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = mma<TY>(qf[i], pf[j], acc[i][j]);
+    }
+    // the stage is read before its next loads go out
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  issue(st0, 0);
+  if (S >= 3) issue(st1, 1);
+  if (S >= 4) issue(st2, 2);
+  for (int k = 0; k < mine; k += S) {
+    if constexpr (S == 2) {
+      issue(st1, k + 1); multiply(st0);
+      issue(st0, k + 2); multiply(st1);
+    } else if constexpr (S == 3) {
+      issue(st2, k + 2); multiply(st0);
+      issue(st0, k + 3); multiply(st1);
+      issue(st1, k + 4); multiply(st2);
+    } else {
+      issue(st3, k + 3); multiply(st0);
+      issue(st0, k + 4); multiply(st1);
+      issue(st1, k + 5); multiply(st2);
+      issue(st2, k + 6); multiply(st3);
+    }
+  }
+
+  stage_barrier();  // every load has landed: the first stage takes the sums
+  acc_t* part = reinterpret_cast<acc_t*>(st0);
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) part[(w * NC * NT + i * NT + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  // fragment f's sum by wave f % 4: lane l holds columns 4 (l / 16) + 0..3 of row l % 16
+  for (int f = w; f < NC * NT; f += kFewWaves) {
+    acc_t sum = part[f * 64 + lane];
+#pragma unroll
+    for (int v = 1; v < kFewWaves; ++v) sum += part[(v * NC * NT + f) * 64 + lane];
+    const int r = (f % NT) * 16 + m, c = n0 + (f / NT) * 16 + 4 * g;
+    if (r >= pl.rows || c >= a.N) continue;
+    store4(a.out, (long(pl.row0) + r) * a.N + c, scaled<TY>(a, pl.e, pl.row0 + r, c, sum), a.out_ty);
+  }
+}
+
+// Row tiles of a launch: sum over non-empty groups (and the tail) of ceil(n / rows) at most.
+long row_tiles(const MmArgs& a, int rows) {
+  const long G = (a.E < a.R ? a.E : a.R) + (a.clear_tail ? 1 : 0);
+  const long most = (long(a.R) + G * (rows - 1)) / rows;
+  return most < a.R ? most : a.R;
+}
+
+// The shape of a launch: rows and columns of a tile; few: k_mm_few.
+struct TileShape {
+  int few, rows, cols;
+};
+
+// The tile shape whose launch brings the fewest bytes through a CU: rounds of
+// one tile per CU times (rows + columns) of a tile.  Times follow that count
+// over the whole range where tiles do not yet fill the chip (H = K = 4096
+// bf16, one matrix: 3 us + 0.165 us per row or column; R=64, N=4096: 16 x 64
+// 14.3 us, 32 x 32 12.6, 64 x 64 22.1, 64 x 256 58; R=1024: 32 x 32 146, 64 x
+// 64 84, 256 x 256 101), and from there on it prefers the large tiles, which
+// the matrix units need.  The row tiles of ragged groups are estimated: groups
+// with a row, each half a tile more than its mean needs.  Among equals the
+// first, so the smaller tiles and k_mm_few (H=4096 to I=1536, 8 tokens
+// top-8 of 64: 94 us against 123).
+TileShape shape_of(int op, const MmArgs& a) {
+  if (op == kWgrad) return {0, 256, kBN};
+  static const TileShape shapes[] = {{1, 16, 64}, {1, 16, 32}, {1, 16, 16}, {1, 32, 32}, {1, 32, 64}, {1, 32, 16},
+                                     {1, 64, 64}, {1, 64, 32}, {1, 64, 16}, {0, 64, kBN}, {0, 128, kBN}, {0, 256, kBN}};
+  const double cols = op == kFwd ? a.N : a.K;
+  const double groups = a.E * (1.0 - std::exp(-double(a.R) / a.E));  // that are touched
+  const double mean = a.R / std::fmax(groups, 1.0);
+  TileShape best = {0, 256, kBN};
+  double least = 1e300;
+  for (const TileShape& s : shapes) {
+    if (s.few && op != kFwd) continue;
+    const double need = mean / s.rows;
+    const double rows = a.E == 1 ? std::ceil(need) : groups * std::fmax(1.0, need + 0.5);
+    const double cost = std::ceil(std::ceil(rows) * std::ceil(cols / s.cols) / kCUs) * (s.rows + s.cols);
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
 }
 
 }  // namespace
 
 long mm_grid(int op, const MmArgs& a) {
-  const int BM = row_tile(op, a);
-  const long cols = op == kFwd ? a.N : a.K, ncol = (cols + kBN - 1) / kBN;
-  long rows;
-  if (op == kWgrad) {
-    rows = long(a.E) * ((a.N + BM - 1) / BM);
-  } else {
-    // sum over non-empty groups (and the tail) of ceil(n / BM)
-    const long G = (a.E < a.R ? a.E : a.R) + (a.clear_tail ? 1 : 0);
-    const long most = (long(a.R) + G * (BM - 1)) / BM;
-    rows = most < a.R ? most : a.R;
-  }
+  const TileShape s = shape_of(op, a);
+  const long cols = op == kFwd ? a.N : a.K, ncol = (cols + s.cols - 1) / s.cols;
+  const long rows = op == kWgrad ? long(a.E) * ((a.N + s.rows - 1) / s.rows) : row_tiles(a, s.rows);
   return (rows * ncol + 7) / 8 * 8;
 }
+
+#define MOE_MM(kernel, threads) hipLaunchKernelGGL((kernel), dim3(grid), dim3(threads), 0, st, a)
 
 template <int OP, int TY>
 static hipError_t launch_bm(const MmArgs& a, hipStream_t st) {
   const unsigned grid = unsigned(mm_grid(OP, a));
+  const TileShape s = shape_of(OP, a);
   if constexpr (OP == kWgrad) {
-    hipLaunchKernelGGL((k_mm<OP, TY, 256>), dim3(grid), dim3(kThreads), 0, st, a);
+    MOE_MM((k_mm<OP, TY, 256>), kThreads);
   } else {
-    const int BM = row_tile(OP, a);
-    if (BM == 256) hipLaunchKernelGGL((k_mm<OP, TY, 256>), dim3(grid), dim3(kThreads), 0, st, a);
-    else if (BM == 128) hipLaunchKernelGGL((k_mm<OP, TY, 128>), dim3(grid), dim3(kThreads), 0, st, a);
-    else hipLaunchKernelGGL((k_mm<OP, TY, 64>), dim3(grid), dim3(kThreads), 0, st, a);
+    if constexpr (OP == kFwd) {
+      if (s.few) {
+        const int v = s.rows / 16 * 16 + s.cols / 16;
+#define MOE_FEW(NT, NC, S) \
+  case NT * 16 + NC: MOE_MM((k_mm_few<TY, NC, NT, S>), kFewWaves * 64); break;
+        switch (v) {
+          MOE_FEW(1, 1, 4) MOE_FEW(1, 2, 3) MOE_FEW(1, 4, 2)
+          MOE_FEW(2, 1, 4) MOE_FEW(2, 2, 2) MOE_FEW(2, 4, 2)
+          MOE_FEW(4, 1, 2) MOE_FEW(4, 2, 3) MOE_FEW(4, 4, 2)
+        }
+#undef MOE_FEW
+        return hipGetLastError();
+      }
+    }
+    if (s.rows == 256) MOE_MM((k_mm<OP, TY, 256>), kThreads);
+    else if (s.rows == 128) MOE_MM((k_mm<OP, TY, 128>), kThreads);
+    else MOE_MM((k_mm<OP, TY, 64>), kThreads);
   }
   return hipGetLastError();
 }
+#undef MOE_MM
 
 hipError_t launch_mm(int op, const MmArgs& a, hipStream_t st) {
   if (mm_grid(op, a) == 0) return hipSuccess;
