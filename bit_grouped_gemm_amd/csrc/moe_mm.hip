@@ -148,18 +148,17 @@ __device__ __forceinline__ typename Acc<TY>::type mma(const v4i& a, const v4i& b
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
-// four fp32 results to the output type, rounded once (to nearest even; NaN
-// and infinity stay)
+// four fp32 results in a 16-bit type, rounded once (to nearest even; NaN and
+// infinity stay)
+__device__ __forceinline__ uint2 round4(const v4f& v, int ty) {
+  typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+  typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+  return ty == kFp16 ? __builtin_bit_cast(uint2, __builtin_convertvector(v, h4))
+                     : __builtin_bit_cast(uint2, __builtin_convertvector(v, b4));
+}
 __device__ __forceinline__ void store4(void* out, long at, const v4f& v, int ty) {
-  if (ty == kFp32) {
-    *reinterpret_cast<v4f*>(static_cast<float*>(out) + at) = v;
-  } else if (ty == kFp16) {
-    typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-    *reinterpret_cast<h4*>(static_cast<_Float16*>(out) + at) = __builtin_convertvector(v, h4);
-  } else {
-    typedef __bf16 b4 __attribute__((ext_vector_type(4)));
-    *reinterpret_cast<b4*>(static_cast<__bf16*>(out) + at) = __builtin_convertvector(v, b4);
-  }
+  if (ty == kFp32) *reinterpret_cast<v4f*>(static_cast<float*>(out) + at) = v;
+  else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = round4(v, ty);
 }
 
 // The result of a sum: itself, or for int8 (sum * token's scale) * channel's
@@ -309,7 +308,10 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
       qs.init(we + long(ct) * kBN * ldp, long(min(kBN, a.N - ct * kBN)) * ldp, ldp, w, lane, nullptr, 0, 0);
     else
       qs.init(we + ct * kBN * 2, (long(a.N) * a.K - ct * kBN) * 2, long(a.K) * 2, w, lane, nullptr, 0, 0);
-    if (pl.e == a.E) red = 0;  // rows behind the last group: zeros
+    if (pl.e == a.E) {  // rows behind the last group: zeros
+      red = 0;
+      qs.left = 0;
+    }
   }
   const int steps = (red + kStep - 1) / kStep;
 
@@ -327,51 +329,108 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
     qs.advance();
     kleft -= 128;
   };
-  auto multiply = [&](const uint8_t* sp, const uint8_t* sq) __attribute__((always_inline)) {
+  // The fragments of half a step.  Each half is read while the half before it
+  // is multiplied, so a step has one barrier, between its halves: by then every
+  // wave has read the whole stage, which the step after next may overwrite, and
+  // the next stage, whose loads went out one step earlier, has arrived.
+  struct Half {
+    v4i p[MF], q[NF];
+  };
+  auto read = [&](Half& f, const uint8_t* sp, const uint8_t* sq, int kk) __attribute__((always_inline)) {
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      v4i pf[MF], qf[NF];
+    for (int j = 0; j < NF; ++j) f.q[j] = read_frag<QT, kBN>(sq, wn * NF + j, kk, lane);
 #pragma unroll
-      for (int j = 0; j < NF; ++j) qf[j] = read_frag<QT, kBN>(sq, wn * NF + j, kk, lane);
+    for (int i = 0; i < MF; ++i) f.p[i] = read_frag<PT, BM>(sp, wm * MF + i, kk, lane);
+  };
+  auto multiply = [&](const Half& f) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < MF; ++i) pf[i] = read_frag<PT, BM>(sp, wm * MF + i, kk, lane);
+    for (int i = 0; i < MF; ++i)
 #pragma unroll
-      for (int i = 0; i < MF; ++i)
+      for (int j = 0; j < NF; ++j) acc[i][j] = mma<TY>(f.q[j], f.p[i], acc[i][j]);
+  };
+  Half even, odd;
+  // one step from stage x, with y the other stage (what is read from it after
+  // the last step goes unused)
+  auto step = [&](uint8_t* px, uint8_t* qx, const uint8_t* py, const uint8_t* qy) __attribute__((always_inline)) {
+    read(odd, px, qx, 1);
+    multiply(even);
+    stage_barrier();
+    issue(px, qx);
+    read(even, py, qy, 0);
+    multiply(odd);
 #pragma unroll
-        for (int j = 0; j < NF; ++j) acc[i][j] = mma<TY>(qf[j], pf[i], acc[i][j]);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < PS::kLoads + QS::kLoads; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, MF * NF / 8, 0);
     }
   };
-
-  // a stage's barrier: its loads have arrived, the other stage is no longer read
-  if (steps > 0) issue(p0, q0);
+  issue(p0, q0);
+  stage_barrier();
+  issue(p1, q1);
+  read(even, p0, q0, 0);
   int s = 0;
   for (; s + 1 < steps; s += 2) {
-    stage_barrier();
-    issue(p1, q1);
-    multiply(p0, q0);
-    stage_barrier();
-    if (s + 2 < steps) issue(p0, q0);
-    multiply(p1, q1);
+    step(p0, q0, p1, q1);
+    step(p1, q1, p0, q0);
   }
-  if (s < steps) {
-    stage_barrier();
-    multiply(p0, q0);
-  }
+  if (s < steps) step(p0, q0, p1, q1);
 
-  // lane l holds column 4 (l / 16) + 0..3 and row l % 16 of each fragment
-  const int m = lane & 15, g = lane >> 4;
+  // Lane l holds columns 4 (l / 16) + 0..3 of row l % 16 of each fragment.
+  // Sixteen rows at a time go through a piece of LDS of the wave's own, so that
+  // a store covers whole rows of its 64 columns (128 or 256 bytes in a line)
+  // instead of 32-byte pieces, and past the caches (268 MB of bf16 gradients, 16
+  // groups of 1024 rows: 318 us, in 32-byte pieces 408, without stores 285).
+  stage_barrier();  // no stage is read or filled any more
+  int el = lane;
+  asm volatile("" : "+v"(el));  // addresses from here on are not formed before the loop, which has no registers for them
+  const int m = el & 15, g = el >> 4;
   const long out_row0 = OP == kWgrad ? long(pl.e) * a.N + pl.row0 : long(pl.row0);
+  const int r0 = wm * (BM / 2), c0 = ct * kBN + wn * 16 * NF;
+  static_assert(QS::kBytes >= kThreads / 64 * 4096, "a piece of 4 KB per wave");
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
-    const int r = wm * (BM / 2) + i * 16 + m;
-    if (r >= pl.rows) continue;
+    uint8_t* piece = (i & 1 ? q1 : q0) + w * 4096;
+    v4f v[NF];
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
-      const int c = ct * kBN + wn * 64 + j * 16 + 4 * g;
-      if (c >= cols) continue;
-      store4(a.out, (out_row0 + r) * cols + c, scaled<TY>(a, pl.e, pl.row0 + r, c, acc[i][j]), a.out_ty);
+      const int r = r0 + i * 16 + m, c = c0 + j * 16 + 4 * g;
+      v[j] = TY == kInt8 && (r >= pl.rows || c >= cols) ? v4f{0.0f, 0.0f, 0.0f, 0.0f}
+                                                        : scaled<TY>(a, pl.e, pl.row0 + r, c, acc[i][j]);
     }
+    // rows of 128 (256) bytes, their 16-byte chunks exchanged by the row's
+    // number so that the 16 rows' equal columns lie on different banks
+    if (a.out_ty == kFp32) {
+#pragma unroll
+      for (int j = 0; j < NF; ++j) *reinterpret_cast<v4f*>(piece + m * 256 + (((4 * j + g) ^ m) << 4)) = v[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < NF; ++j)
+        *reinterpret_cast<uint2*>(piece + m * 128 + (((2 * j + (g >> 1)) ^ (m & 7)) << 4) + (g & 1) * 8) =
+            round4(v[j], a.out_ty);
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (a.out_ty == kFp32) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int row = h * 4 + (el >> 4), ch = el & 15;
+        const v4i d = *reinterpret_cast<const v4i*>(piece + row * 256 + ((ch ^ row) << 4));
+        const int r = r0 + i * 16 + row, c = c0 + ch * 4;
+        if (r < pl.rows && c < cols)
+          __builtin_nontemporal_store(d, reinterpret_cast<v4i*>(static_cast<float*>(a.out) + (out_row0 + r) * cols + c));
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = h * 8 + (el >> 3), ch = el & 7;
+        const v4i d = *reinterpret_cast<const v4i*>(piece + row * 128 + ((ch ^ (row & 7)) << 4));
+        const int r = r0 + i * 16 + row, c = c0 + ch * 8;
+        if (r < pl.rows && c < cols)
+          __builtin_nontemporal_store(d,
+                                      reinterpret_cast<v4i*>(static_cast<uint16_t*>(a.out) + (out_row0 + r) * cols + c));
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
