@@ -59,7 +59,8 @@ EXPORTS = ("moe_workspace_size", "moe_permute", "moe_grouped_gemm1_swiglu", "moe
            "moe_prepack_weights",
            "moe_stream_read",
            "moe_mfma_rate", "moe_encode_e4m3", "moe_route", "moe_route_workspace_size", "moe_status_str",
-           "moe_grouped_mm", "moe_grouped_mm_dgrad", "moe_grouped_mm_wgrad", "moe_quant_i8", "moe_mm_i8",
+           "moe_grouped_mm", "moe_grouped_mm_dgrad", "moe_grouped_mm_wgrad",
+           "moe_grouped_mm_wgrad_workspace_size", "moe_quant_i8", "moe_mm_i8",
            "moe_linear_i8", "moe_linear_i8_workspace_size")
 
 # element types of the row-major products
@@ -119,7 +120,8 @@ def load(path: str = LIB_PATH) -> C.CDLL:
     mmp = C.POINTER(MoeMmCfg)
     L.moe_grouped_mm.argtypes = [mmp, vp, vp, vp, vp, vp]
     L.moe_grouped_mm_dgrad.argtypes = [mmp, vp, vp, vp, vp, vp]
-    L.moe_grouped_mm_wgrad.argtypes = [mmp, vp, vp, vp, vp, vp]
+    L.moe_grouped_mm_wgrad.argtypes = [mmp, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_grouped_mm_wgrad_workspace_size.argtypes = [mmp, C.POINTER(sz)]
     L.moe_quant_i8.argtypes = [C.c_int, C.c_int, C.c_int, C.c_int, vp, vp, vp, vp]
     L.moe_mm_i8.argtypes = [mmp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.moe_linear_i8_workspace_size.argtypes = [mmp, C.c_int, C.POINTER(sz)]
@@ -489,10 +491,13 @@ def moe_grouped_mm_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tenso
 
 
 def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
-                         out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+                         out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                         work: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dw [E, N, K] = dy[r]^T x[r] summed over the rows r of each group e (zeros
     for an empty group): moe_grouped_mm's gradient with respect to w.
-    `out_dtype`: dy's (default) or torch.float32; `out` is fully overwritten."""
+    `out_dtype`: dy's (default) or torch.float32; `out` is fully overwritten.
+    `work`: uint8 scratch of at least moe_grouped_mm_wgrad_workspace_size(...)
+    bytes, allocated where absent and needed."""
     (R, N), K, dt, dev = _rows_of("dy", dy), _rows_of("x", x)[1], dy.dtype, dy.device
     if offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError(f"offsets: shape {tuple(offsets.shape)}, expected (E + 1,)")
@@ -506,8 +511,24 @@ def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     out, _ = _new_or_checked(out, (E, N, K), out_dtype or dt, allowed, dev)
     pw = _addr("out", out, allowed, (E, N, K), dev)
     c = MoeMmCfg(R, N, K, E, 0, _DT[dt], _DT[out.dtype], 0)
-    _call("moe_grouped_mm_wgrad", dev.index, C.byref(c), pd, px, po, pw)
+    if work is None:
+        need = _wgrad_bytes(c)
+        work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    pk = None if work is None else _addr("work", work, (torch.uint8,), work.shape, dev)
+    _call("moe_grouped_mm_wgrad", dev.index, C.byref(c), pd, px, po, pw, pk, 0 if work is None else work.numel())
     return out
+
+
+def _wgrad_bytes(c: MoeMmCfg) -> int:
+    n = C.c_size_t(0)
+    _check("moe_grouped_mm_wgrad_workspace_size",
+           (_lib or load()).moe_grouped_mm_wgrad_workspace_size(C.byref(c), C.byref(n)))
+    return n.value
+
+
+def moe_grouped_mm_wgrad_workspace_size(R: int, N: int, K: int, E: int) -> int:
+    """Bytes of scratch moe_grouped_mm_wgrad needs for dy [R, N], x [R, K] and E groups."""
+    return _wgrad_bytes(MoeMmCfg(R, N, K, E, 0, 0, 0, 0))
 
 
 class _GroupedMM(torch.autograd.Function):

@@ -30,8 +30,12 @@ struct MmArgs {
   int ty;                    // operand type
   int out_ty;                // output type
   int clear_tail;            // rows behind the last group: 1 written as zeros, 0 left alone
+  float* partial;            // kWgrad: wgrad_bytes() of scratch, or null where that is 0
+  int splits;                // set by launch_mm
 };
 
+// Scratch of kWgrad.
+size_t wgrad_bytes(const MmArgs& a);
 // Number of workgroups of a launch (64-bit: the ABI refuses more than 2^31).
 long mm_grid(int op, const MmArgs& a);
 hipError_t launch_mm(int op, const MmArgs& a, hipStream_t st);

@@ -272,26 +272,29 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
   const int ncol = (cols + kBN - 1) / kBN;
 
   Place pl;
-  int ct, red;  // column tile, reduction length
+  int ct, red, split = 0;  // column tile, reduction length, share of the group's rows
   PS ps;
   QS qs;
   const uint8_t* P = static_cast<const uint8_t*>(a.p);
   const uint8_t* Q = static_cast<const uint8_t*>(a.q);
   if constexpr (OP == kWgrad) {
-    // tile of group e: rows are N, columns K; XCD x takes a run of tiles
-    const int nrow = (a.N + BM - 1) / BM;
-    const long tiles = long(a.E) * nrow * ncol, per = (tiles + 7) / 8;
-    const long t = long(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if (long(blockIdx.x >> 3) >= per || t >= tiles) return;
-    pl.e = int(t / (long(nrow) * ncol));
-    const int in = int(t - long(pl.e) * nrow * ncol);
-    ct = in / nrow;
-    const int rt = in % nrow;
-    pl.row0 = rt * BM;
+    // tile of group e: rows are N, columns K; XCD x takes a run of tiles.  A
+    // group's rows may be split over a.splits workgroups, in whole steps.
+    const uint32_t nrow = (a.N + BM - 1) / BM, one = nrow * ncol;
+    const uint32_t tiles = a.E * a.splits * one, per = (tiles + 7) / 8;
+    const uint32_t t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= per || t >= tiles) return;
+    const uint32_t part = t / one, in = t - part * one;
+    pl.e = int(part / a.splits);
+    split = int(part - pl.e * uint32_t(a.splits));
+    ct = int(in / nrow);
+    pl.row0 = int(in % nrow) * BM;
     pl.rows = min(BM, a.N - pl.row0);
     const int2 r = group_rows(a.offsets, pl.e, a.E, a.R);
-    const int ra = __builtin_amdgcn_readfirstlane(r.x);
-    red = __builtin_amdgcn_readfirstlane(r.y) - ra;
+    const int all = r.y - r.x, each = ((all + kStep - 1) / kStep + a.splits - 1) / a.splits * kStep;
+    const int skip = int(min(long(split) * each, long(all)));
+    const int ra = __builtin_amdgcn_readfirstlane(r.x + skip);
+    red = __builtin_amdgcn_readfirstlane(min(each, all - skip));
     ps.init(P + (long(ra) * a.N + pl.row0) * 2, (long(red) * a.N - pl.row0) * 2, long(a.N) * 2, w, lane, nullptr, 0, 0);
     qs.init(Q + (long(ra) * a.K + ct * kBN) * 2, (long(red) * a.K - ct * kBN) * 2, long(a.K) * 2, w, lane, nullptr, 0,
             0);
@@ -386,6 +389,8 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
   asm volatile("" : "+v"(el));  // addresses from here on are not formed before the loop, which has no registers for them
   const int m = el & 15, g = el >> 4;
   const long out_row0 = OP == kWgrad ? long(pl.e) * a.N + pl.row0 : long(pl.row0);
+  const int out_ty = OP == kWgrad && a.splits > 1 ? kFp32 : a.out_ty;
+  void* out = OP == kWgrad && a.splits > 1 ? a.partial + long(split) * a.E * a.N * a.K : a.out;
   const int r0 = wm * (BM / 2), c0 = ct * kBN + wn * 16 * NF;
   static_assert(QS::kBytes >= kThreads / 64 * 4096, "a piece of 4 KB per wave");
 #pragma unroll
@@ -400,24 +405,24 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
     }
     // rows of 128 (256) bytes, their 16-byte chunks exchanged by the row's
     // number so that the 16 rows' equal columns lie on different banks
-    if (a.out_ty == kFp32) {
+    if (out_ty == kFp32) {
 #pragma unroll
       for (int j = 0; j < NF; ++j) *reinterpret_cast<v4f*>(piece + m * 256 + (((4 * j + g) ^ m) << 4)) = v[j];
     } else {
 #pragma unroll
       for (int j = 0; j < NF; ++j)
         *reinterpret_cast<uint2*>(piece + m * 128 + (((2 * j + (g >> 1)) ^ (m & 7)) << 4) + (g & 1) * 8) =
-            round4(v[j], a.out_ty);
+            round4(v[j], out_ty);
     }
     __builtin_amdgcn_wave_barrier();
-    if (a.out_ty == kFp32) {
+    if (out_ty == kFp32) {
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         const int row = h * 4 + (el >> 4), ch = el & 15;
         const v4i d = *reinterpret_cast<const v4i*>(piece + row * 256 + ((ch ^ row) << 4));
         const int r = r0 + i * 16 + row, c = c0 + ch * 4;
         if (r < pl.rows && c < cols)
-          __builtin_nontemporal_store(d, reinterpret_cast<v4i*>(static_cast<float*>(a.out) + (out_row0 + r) * cols + c));
+          __builtin_nontemporal_store(d, reinterpret_cast<v4i*>(static_cast<float*>(out) + (out_row0 + r) * cols + c));
       }
     } else {
 #pragma unroll
@@ -427,7 +432,7 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
         const int r = r0 + i * 16 + row, c = c0 + ch * 8;
         if (r < pl.rows && c < cols)
           __builtin_nontemporal_store(d,
-                                      reinterpret_cast<v4i*>(static_cast<uint16_t*>(a.out) + (out_row0 + r) * cols + c));
+                                      reinterpret_cast<v4i*>(static_cast<uint16_t*>(out) + (out_row0 + r) * cols + c));
       }
     }
     __builtin_amdgcn_wave_barrier();
@@ -567,6 +572,23 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_mm_few(MmArgs a) {
   }
 }
 
+// dw = the splits' fp32 sums added up in their order.
+__global__ __launch_bounds__(256) void k_join(const float* __restrict__ part, int splits, long n, void* out, int ty) {
+  for (long i = (long(blockIdx.x) * 256 + threadIdx.x) * 4; i < n; i += long(gridDim.x) * 1024) {
+    v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    int s = 0;
+    for (; s + 8 <= splits; s += 8) {  // eight loads in flight
+      v4f v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const v4f*>(part + (s + u) * n + i);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) sum += v[u];
+    }
+    for (; s < splits; ++s) sum += *reinterpret_cast<const v4f*>(part + s * n + i);
+    store4(out, i, sum, ty);
+  }
+}
+
 // Row tiles of a launch: sum over non-empty groups (and the tail) of ceil(n / rows) at most.
 long row_tiles(const MmArgs& a, int rows) {
   const long G = (a.E < a.R ? a.E : a.R) + (a.clear_tail ? 1 : 0);
@@ -589,7 +611,7 @@ struct TileShape {
 // with a row, each half a tile more than its mean needs.  Among equals the
 // first, so the smaller tiles and k_mm_few (H=4096 to I=1536, 8 tokens
 // top-8 of 64: 94 us against 123).
-TileShape shape_of(int op, const MmArgs& a) {
+TileShape shape_of(int op, const MmArgs& a, double* cost_of = nullptr) {
   if (op == kWgrad) return {0, 256, kBN};
   static const TileShape shapes[] = {{1, 16, 64}, {1, 16, 32}, {1, 16, 16}, {1, 32, 32}, {1, 32, 64}, {1, 32, 16},
                                      {1, 64, 64}, {1, 64, 32}, {1, 64, 16}, {0, 64, kBN}, {0, 128, kBN}, {0, 256, kBN}};
@@ -601,22 +623,59 @@ TileShape shape_of(int op, const MmArgs& a) {
   for (const TileShape& s : shapes) {
     if (s.few && op != kFwd) continue;
     const double need = mean / s.rows;
-    const double rows = a.E == 1 ? std::ceil(need) : groups * std::fmax(1.0, need + 0.5);
+    const double rows = a.E == 1 ? std::ceil(a.R / double(s.rows)) : groups * std::fmax(1.0, need + 0.5);
     const double cost = std::ceil(std::ceil(rows) * std::ceil(cols / s.cols) / kCUs) * (s.rows + s.cols);
     if (cost < least) {
       least = cost;
       best = s;
     }
   }
+  if (cost_of) *cost_of = least;
   return best;
+}
+
+// Rows of a dense product's first launch.  Where the last few rows would make
+// the large tiles go one more round, they go into a launch of their own, in the
+// shape that suits them (int8, 4099 rows, K = 7168, N = 4096, quantised: 180 us in
+// one launch, 121 in two); a launch counts as much as bringing in kLaunchBytes.
+constexpr double kLaunchBytes = 150e3;
+int first_rows(int op, const MmArgs& a) {
+  if (op != kFwd || a.offsets || a.R <= 256) return a.R;
+  double one, head, tail;
+  const int el = a.ty == kInt8 ? 1 : 2;
+  shape_of(op, a, &one);
+  const int rows = a.R / 256 * 256;
+  MmArgs h = a, t = a;
+  h.R = rows;
+  t.R = a.R - rows;
+  if (!t.R) return a.R;
+  shape_of(op, h, &head);
+  shape_of(op, t, &tail);
+  return head + tail + kLaunchBytes / (double(a.K) * el) < one ? rows : a.R;
+}
+
+// Workgroups that share a group's rows in kWgrad: as many as leave the chip one
+// tile per CU, while each keeps eight steps of 64 rows.  Their fp32 sums meet
+// in a workspace and are added up in order.  (One matrix of 512 x 512 from
+// 32768 rows: 521 us unsplit, 41 split.)
+int splits_of(const MmArgs& a) {
+  const double tiles = double(a.E) * ((a.N + 255) / 256) * ((a.K + kBN - 1) / kBN);
+  const double steps = a.R / 64.0 / a.E;
+  return int(std::fmax(1.0, std::fmin(std::floor(kCUs / tiles), std::floor(steps / 8))));
 }
 
 }  // namespace
 
+size_t wgrad_bytes(const MmArgs& a) {
+  const int s = splits_of(a);
+  return s > 1 ? size_t(s) * a.E * a.N * a.K * 4 : 0;
+}
+
 long mm_grid(int op, const MmArgs& a) {
   const TileShape s = shape_of(op, a);
   const long cols = op == kFwd ? a.N : a.K, ncol = (cols + s.cols - 1) / s.cols;
-  const long rows = op == kWgrad ? long(a.E) * ((a.N + s.rows - 1) / s.rows) : row_tiles(a, s.rows);
+  const long rows =
+      op == kWgrad ? long(a.E) * splits_of(a) * ((a.N + s.rows - 1) / s.rows) : row_tiles(a, s.rows);
   return (rows * ncol + 7) / 8 * 8;
 }
 
@@ -628,6 +687,11 @@ static hipError_t launch_bm(const MmArgs& a, hipStream_t st) {
   const TileShape s = shape_of(OP, a);
   if constexpr (OP == kWgrad) {
     MOE_MM((k_mm<OP, TY, 256>), kThreads);
+    if (a.splits > 1) {
+      const long n = long(a.E) * a.N * a.K, blocks = (n + 1023) / 1024;
+      hipLaunchKernelGGL(k_join, dim3(unsigned(blocks < 2048 ? blocks : 2048)), dim3(256), 0, st, a.partial, a.splits, n,
+                         a.out, a.out_ty);
+    }
   } else {
     if constexpr (OP == kFwd) {
       if (s.few) {
@@ -651,7 +715,7 @@ static hipError_t launch_bm(const MmArgs& a, hipStream_t st) {
 }
 #undef MOE_MM
 
-hipError_t launch_mm(int op, const MmArgs& a, hipStream_t st) {
+static hipError_t launch_one(int op, const MmArgs& a, hipStream_t st) {
   if (mm_grid(op, a) == 0) return hipSuccess;
   if (a.ty == kInt8) return launch_bm<kFwd, kInt8>(a, st);
   if (a.ty == kBf16)
@@ -659,6 +723,26 @@ hipError_t launch_mm(int op, const MmArgs& a, hipStream_t st) {
                       : op == kDgrad ? launch_bm<kDgrad, kBf16>(a, st) : launch_bm<kWgrad, kBf16>(a, st);
   return op == kFwd ? launch_bm<kFwd, kFp16>(a, st)
                     : op == kDgrad ? launch_bm<kDgrad, kFp16>(a, st) : launch_bm<kWgrad, kFp16>(a, st);
+}
+
+hipError_t launch_mm(int op, const MmArgs& args, hipStream_t st) {
+  MmArgs a = args;
+  a.splits = op == kWgrad ? splits_of(a) : 1;
+  const int rows = first_rows(op, a);
+  if (rows == a.R) return launch_one(op, a, st);
+  MmArgs head = a, tail = a;
+  const long el = a.ty == kInt8 ? 1 : 2, out_el = a.out_ty == kFp32 ? 4 : 2;
+  head.R = rows;
+  tail.R = a.R - rows;
+  tail.out = static_cast<uint8_t*>(a.out) + long(rows) * a.N * out_el;
+  if (a.row_token) {
+    tail.row_token = a.row_token + rows;
+  } else {
+    tail.p = static_cast<const uint8_t*>(a.p) + long(rows) * a.K * el;
+    if (a.ps) tail.ps = a.ps + rows;
+  }
+  const hipError_t e = launch_one(op, head, st);
+  return e != hipSuccess ? e : launch_one(op, tail, st);
 }
 
 }  // namespace moe

@@ -70,14 +70,19 @@ int enqueue(int op, const MmArgs& a, void* stream) {
 }
 
 int grouped(int op, const moe_mm_cfg* c, const void* p, const void* q, const int32_t* offsets, void* out,
-            bool p_rows, bool q_rows, bool out_rows, void* stream) {
+            bool p_rows, bool q_rows, bool out_rows, void* stream, void* work = nullptr, size_t work_bytes = 0) {
   if (!c) return MOE_ERR_NULL_ARG;
   const bool some = c->R != 0;  // operands with one row per R may be null where there is none
   int rc;
   if ((rc = null_ptrs({{p, some || !p_rows}, {q, some || !q_rows}, {offsets, true}, {out, some || !out_rows}}))) return rc;
   if ((rc = check_dims(c)) || (rc = check_types(c))) return rc;
-  if ((rc = misaligned_ptrs({{p, true}, {q, true}, {offsets, true}, {out, true}}))) return rc;
-  return enqueue(op, args_of(c, p, q, offsets, out), stream);
+  if ((rc = misaligned_ptrs({{p, true}, {q, true}, {offsets, true}, {out, true}, {work, true}}))) return rc;
+  MmArgs a = args_of(c, p, q, offsets, out);
+  const size_t need = op == kWgrad ? wgrad_bytes(a) : 0;
+  if (need && !work) return MOE_ERR_NULL_ARG;
+  if (need > work_bytes) return MOE_ERR_WORKSPACE;
+  a.partial = static_cast<float*>(work);
+  return enqueue(op, a, stream);
 }
 
 }  // namespace
@@ -92,9 +97,17 @@ extern "C" int moe_grouped_mm_dgrad(const moe_mm_cfg* cfg, const void* dy, const
   return grouped(kDgrad, cfg, dy, w, offsets, dx, true, false, true, stream);
 }
 
+extern "C" int moe_grouped_mm_wgrad_workspace_size(const moe_mm_cfg* cfg, size_t* bytes) {
+  if (!cfg || !bytes) return MOE_ERR_NULL_ARG;
+  int rc;
+  if ((rc = check_dims(cfg)) || (rc = check_types(cfg))) return rc;
+  *bytes = wgrad_bytes(args_of(cfg, nullptr, nullptr, nullptr, nullptr));
+  return MOE_OK;
+}
+
 extern "C" int moe_grouped_mm_wgrad(const moe_mm_cfg* cfg, const void* dy, const void* x, const int32_t* offsets,
-                                    void* dw, void* stream) {
-  return grouped(kWgrad, cfg, dy, x, offsets, dw, true, true, false, stream);
+                                    void* dw, void* work, size_t work_bytes, void* stream) {
+  return grouped(kWgrad, cfg, dy, x, offsets, dw, true, true, false, stream, work, work_bytes);
 }
 
 extern "C" int moe_quant_i8(int R, int K, int dtype, int swiglu, const void* x, int8_t* codes, float* scales,

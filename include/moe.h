@@ -372,9 +372,14 @@ int moe_grouped_mm_dgrad(const moe_mm_cfg* cfg, const void* dy, const void* w, c
 /* The gradient with respect to w: dw[e][n][k] = sum over the rows r of group
  * e of dy[r][n] * x[r][k]; zeros for an empty group.
  *   dy [R][N], x [R][K] of dtype; dw [E][N][K] of out_dtype, fully
- *   overwritten.  The sum's order is fixed: equal inputs give equal bits. */
+ *   overwritten.  The sum's order is fixed: equal inputs give equal bits.
+ *   work: device scratch of moe_grouped_mm_wgrad_workspace_size(cfg) bytes
+ *   (contents on entry ignored; NULL when that size is 0), where the rows of
+ *   few and small matrices are split over several workgroups whose fp32 sums
+ *   meet there. */
+int moe_grouped_mm_wgrad_workspace_size(const moe_mm_cfg* cfg, size_t* bytes);
 int moe_grouped_mm_wgrad(const moe_mm_cfg* cfg, const void* dy, const void* x, const int32_t* offsets, void* dw,
-                         void* stream);
+                         void* work, size_t work_bytes, void* stream);
 
 /* Per-token int8 quantisation (the FusedDeepMoE analysis's QuantToken): for
  * each row v of K values, a = max |v|, m = 127 / max(a, 2^-64) (fp32,

@@ -105,6 +105,8 @@ SHAPES = {
     "skewed": ([900] + [0] * 30 + [1], 0, 256, 128),
     "many_groups": ([i % 5 for i in range(200)], 9, 64, 64),
     "long_k": ([2, 30], 0, 16, 8200),
+    "rows_split_for_dw": ([3000, 0, 1511], 70, 72, 136),
+    "rows_split_for_one_dw": ([33001], 0, 136, 264),
     "decode_slice": ([1, 0, 2, 1, 0, 0, 3, 1], 0, 1536, 4096),
 }
 
@@ -335,7 +337,7 @@ def test_mm_i8_grouped(name, od):
 
 
 @pytest.mark.parametrize("R,N,K", [(1, 8, 16), (1, 4096, 7168), (3, 520, 1008), (17, 264, 272), (129, 136, 2048),
-                                   (1030, 264, 144)])
+                                   (1030, 264, 144), (4099, 4096, 1024)])  # the last one in two launches
 def test_mm_i8_dense(R, N, K):
     moe = M()
     g = gen(29)
@@ -343,6 +345,10 @@ def test_mm_i8_dense(R, N, K):
     wq, ws = codes(g, N, K), torch.rand(N, device=DEV, generator=g) * 1e-3
     ref = (xq.double() @ wq.double().t()) * xs[:, None].double() * ws.double()
     near_i8(moe.moe_mm_i8(xq, xs, wq, ws, out_dtype=FP32), ref, "dense")
+    t = torch.randint(-1, R + 1, (R,), device=DEV, generator=g).to(torch.int32)
+    ok = (t >= 0) & (t < R)
+    got = moe.moe_mm_i8(xq, xs, wq, ws, row_token=t, out_dtype=FP32)
+    near_i8(got, ref[t.long().clamp(0, R - 1)] * ok[:, None], "gathered")
 
 
 def test_mm_i8_largest_sums():

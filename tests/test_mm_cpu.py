@@ -30,7 +30,8 @@ GROUPED = ("moe_grouped_mm", "moe_grouped_mm_dgrad", "moe_grouped_mm_wgrad")
 
 @pytest.mark.parametrize("name", GROUPED)
 def test_grouped_refusals(name):
-    call = lambda c, p=FAKE, q=FAKE, o=FAKE, out=FAKE: moe.raw_call(name, c, p, q, o, out, None)
+    work = (None, 0) if name == "moe_grouped_mm_wgrad" else ()
+    call = lambda c, p=FAKE, q=FAKE, o=FAKE, out=FAKE: moe.raw_call(name, c, p, q, o, out, *work, None)
     assert call(None) == moe.MOE_ERR_NULL_ARG
     for kw in (dict(p=None), dict(q=None), dict(o=None), dict(out=None)):
         assert call(cfg(), **kw) == moe.MOE_ERR_NULL_ARG, kw
@@ -50,6 +51,24 @@ def test_grouped_refuses_more_workgroups_than_a_launch_has():
     # 2^31 - 1 rows of 2^20 outputs: the tile count passes 2^31
     assert moe.raw_call("moe_grouped_mm", cfg(R=(1 << 31) - 1, N=1 << 20, E=1), FAKE, FAKE, FAKE, FAKE,
                         None) == moe.MOE_ERR_BAD_SHAPE
+
+
+def test_wgrad_workspace():
+    """Few small matrices split their rows and need scratch; many tiles or few rows need none."""
+    n = C.c_size_t(0)
+    size = lambda c: moe.raw_call("moe_grouped_mm_wgrad_workspace_size", c, C.byref(n))
+    assert size(cfg(R=1 << 15, N=512, K=512, E=1)) == moe.MOE_OK and n.value == 64 * 512 * 512 * 4
+    need = n.value
+    for kw in (dict(R=1 << 15, N=4096, K=4096, E=1), dict(R=512, N=512, K=512, E=1), dict(R=0, E=1)):
+        assert size(cfg(**kw)) == moe.MOE_OK and n.value == 0, kw
+    assert size(None) == moe.MOE_ERR_NULL_ARG
+    assert moe.raw_call("moe_grouped_mm_wgrad_workspace_size", cfg(), None) == moe.MOE_ERR_NULL_ARG
+    assert size(cfg(N=4)) == moe.MOE_ERR_BAD_SHAPE and size(cfg(dtype=2, out_dtype=2)) == moe.MOE_ERR_UNSUPPORTED
+    call = lambda work, nb: moe.raw_call("moe_grouped_mm_wgrad", cfg(R=1 << 15, N=512, K=512, E=1), FAKE, FAKE, FAKE,
+                                         FAKE, work, nb, None)
+    assert call(None, need) == moe.MOE_ERR_NULL_ARG
+    assert call(FAKE, need - 1) == moe.MOE_ERR_WORKSPACE
+    assert call(FAKE + 8, need) == moe.MOE_ERR_MISALIGNED
 
 
 def test_quant_refusals():
