@@ -634,11 +634,17 @@ def moe_mm_i8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Te
     return out
 
 
-def moe_linear_i8_workspace_size(rows: int, K: int) -> int:
-    """Bytes of scratch moe_linear_i8 needs for x of `rows` rows and K inputs of w."""
-    n, c = C.c_size_t(0), MoeMmCfg(rows, 8, K, 1, rows, 0, 0, 0)
-    _check("moe_linear_i8_workspace_size", load().moe_linear_i8_workspace_size(C.byref(c), 0, C.byref(n)))
-    return int(n.value)
+def _linear_bytes(c: MoeMmCfg, gathered: int) -> int:
+    n = C.c_size_t(0)
+    _check("moe_linear_i8_workspace_size", (_lib or load()).moe_linear_i8_workspace_size(C.byref(c), gathered, C.byref(n)))
+    return n.value
+
+
+def moe_linear_i8_workspace_size(rows: int, K: int, out_rows: Optional[int] = None) -> int:
+    """Bytes of scratch moe_linear_i8 needs for x of `rows` rows, K inputs of w
+    and, with row_token, `out_rows` rows of the result."""
+    return _linear_bytes(MoeMmCfg(rows if out_rows is None else out_rows, 8, K, 1, rows, 0, 0, 0),
+                         int(out_rows is not None))
 
 
 def moe_linear_i8(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets: Optional[torch.Tensor] = None,
@@ -647,7 +653,7 @@ def moe_linear_i8(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets: 
     """moe_mm_i8 of moe_quant_i8(x, swiglu): 16-bit activations (bfloat16 or
     float16) times int8 weights.  The result has x's type unless out_dtype or
     `out` says otherwise.  `work`: uint8 scratch of at least
-    moe_linear_i8_workspace_size(x.shape[0], K) bytes, allocated where absent."""
+    moe_linear_i8_workspace_size(...) bytes, allocated where absent and needed."""
     (T, _), dev = _rows_of("x", x), x.device
     E, N, K, pw, pws, po = _i8_weights(wq, ws, offsets, dev)
     px = _addr("x", x, _16BIT, (T, 2 * K if swiglu else K), dev)
@@ -658,9 +664,11 @@ def moe_linear_i8(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets: 
     py = _addr("out", out, tuple(_DT), (R, N), dev)
     c = MoeMmCfg(R, N, K, E, T, _DT[x.dtype], _DT[out.dtype], clear)
     if work is None:
-        work = torch.empty(moe_linear_i8_workspace_size(T, K), dtype=torch.uint8, device=dev)
-    pk = _addr("work", work, (torch.uint8,), work.shape, dev)
-    _call("moe_linear_i8", dev.index, C.byref(c), px, int(bool(swiglu)), pw, pws, po, pt, py, pk, work.numel())
+        need = _linear_bytes(c, int(row_token is not None))
+        work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    pk = None if work is None else _addr("work", work, (torch.uint8,), work.shape, dev)
+    _call("moe_linear_i8", dev.index, C.byref(c), px, int(bool(swiglu)), pw, pws, po, pt, py, pk,
+          0 if work is None else work.numel())
     return out
 
 

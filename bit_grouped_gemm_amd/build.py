@@ -11,7 +11,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmoe.so")
 SOURCES = ["moe_api.hip", "moe_kernels.hip", "moe_gemm_big.hip", "moe_tile.hip", "moe_diag.hip", "moe_router.hip",
            "moe_mm_api.hip", "moe_mm.hip", "moe_quant_i8.hip"]
-HEADERS = ["moe_device.h", "moe_launch.h", "moe_mm.h", os.path.join("..", "..", "include", "moe.h")]
+HEADERS = ["moe_device.h", "moe_launch.h", "moe_mm.h", "moe_quant_i8.h", os.path.join("..", "..", "include", "moe.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -40,6 +40,11 @@ size_t wgrad_bytes(const MmArgs& a);
 long mm_grid(int op, const MmArgs& a);
 hipError_t launch_mm(int op, const MmArgs& a, hipStream_t st);
 
+// moe_linear_i8 of one row as one launch: whether it is, and the launch (a.p:
+// the 16-bit rows of type x_ty).
+bool linear_is_one_launch(int R, int K);
+hipError_t launch_linear_one(const MmArgs& a, int x_ty, int swiglu, hipStream_t st);
+
 // Per-token int8 quantisation of rows of `ty` (kBf16 / kFp16): K values per
 // row, or SwiGLU of 2 K (gate first).
 hipError_t launch_quant_i8(const void* x, int ty, int swiglu, int R, int K, int8_t* codes, float* scales,

@@ -22,13 +22,13 @@
 
 #include "moe_device.h"
 #include "moe_mm.h"
+#include "moe_quant_i8.h"
 
 namespace moe {
 namespace {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef short s4v __attribute__((ext_vector_type(4)));
-typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 512;
 constexpr int kBN = 256;     // output columns of a tile
@@ -58,6 +58,16 @@ __device__ __forceinline__ void stage_barrier() {
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Barrier after this wave's LDS accesses; loads stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
@@ -572,6 +582,128 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_mm_few(MmArgs a) {
   }
 }
 
+// moe_linear_i8 for one row: k_mm_few with the quantiser in front, in every
+// workgroup: its lanes hold the row between the maximum and the rounding while
+// the first weights are on their way; the codes stay in LDS, where all K steps
+// read them.  Codes, sums and results are those of the two launches it stands
+// for.  7168 -> 4096: 10.3 us as two launches, 7.9 as one (two rows this
+// way: 12.2 against 11.0, so from there on it is two).
+constexpr int kLinChunks = 4;  // chunks of 8 values that a lane keeps
+constexpr int kLinMaxK = kLinChunks * kFewWaves * 64 * 8;
+
+template <int XT, bool GLU, int NC>
+__global__ __launch_bounds__(kFewWaves * 64) void k_linear_one(MmArgs a) {
+  constexpr int S = 4, L = 2 * NC, kStage = L * 1024;
+  __shared__ __align__(1024) uint8_t st0[kFewWaves * kStage];
+  __shared__ __align__(1024) uint8_t st1[kFewWaves * kStage];
+  __shared__ __align__(1024) uint8_t st2[kFewWaves * kStage];
+  __shared__ __align__(1024) uint8_t st3[kFewWaves * kStage];
+  __shared__ __align__(16) uint8_t codes[kLinMaxK];
+  __shared__ uint32_t s_top[kFewWaves];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = lane & 15, g = lane >> 4;
+  const int ncol = (a.N + 16 * NC - 1) / (16 * NC);
+  Place pl;
+  int ct;
+  if (!find_tile(a, 16, ncol, blockIdx.x, pl, ct)) return;
+  const int K = a.K, n0 = ct * 16 * NC;
+  const bool grouped = pl.e < a.E;  // else the row is behind the last group: zeros
+  const int steps = grouped ? (K + 127) / 128 : 0;
+  const int each = (steps + kFewWaves - 1) / kFewWaves;
+  const int s0 = w * each, mine = max(0, min(steps - s0, each));
+  const uint8_t* wq = static_cast<const uint8_t*>(a.q) + (long(pl.e) * a.N + n0) * K;
+  const uint32_t wspan = uint32_t(min(16 * NC, a.N - n0)) * uint32_t(K);
+  const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+  uint32_t ow[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) ow[i] = uint32_t(8 * i + (lane >> 3)) * uint32_t(K) + chunk;
+  auto issue = [&](uint8_t* stage, int k) __attribute__((always_inline)) {
+    const int at = (s0 + k) * 128;
+    const bool in = k < mine && chunk < K - at;
+#pragma unroll
+    for (int i = 0; i < L; ++i) dma16<true>(wq, wspan, in ? ow[i] + at : kOutside, stage + w * kStage + i * 1024);
+  };
+
+  // the row comes in ahead of the first weights; one that names no token is zeros
+  const int t = a.row_token ? a.row_token[pl.row0] : pl.row0;
+  const bool token = grouped && (!a.row_token || (t >= 0 && t < a.T));
+  const uint16_t* x = static_cast<const uint16_t*>(a.p) + long(token ? t : 0) * (GLU ? 2L * K : K);
+  quant_raw8 raw[kLinChunks][GLU ? 2 : 1];
+#pragma unroll
+  for (int i = 0; i < kLinChunks; ++i) {
+    const int c = (i * kFewWaves * 64 + int(threadIdx.x)) * 8;
+#pragma unroll
+    for (int h = 0; h < (GLU ? 2 : 1); ++h)
+      raw[i][h] = token && c < K ? *reinterpret_cast<const quant_raw8*>(x + h * K + c) : quant_raw8{0, 0, 0, 0};
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  issue(st0, 0);
+  issue(st1, 1);
+  issue(st2, 2);
+  __builtin_amdgcn_sched_barrier(0);
+  f8v v[kLinChunks];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kLinChunks; ++i) {
+    v[i] = quant_value8<XT, GLU>(raw[i][0], raw[i][GLU ? 1 : 0]);
+    top = max(top, quant_top8(v[i]));
+  }
+  for (int d = 1; d < 64; d <<= 1) top = max(top, uint32_t(__shfl_xor(int(top), d, 64)));
+  if (lane == 0) s_top[w] = top;
+  lds_barrier();
+  const QuantScale q = quant_scale(max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3])));
+#pragma unroll
+  for (int i = 0; i < kLinChunks; ++i) {
+    const int c = (i * kFewWaves * 64 + int(threadIdx.x)) * 8;
+    // the last step's columns past K are zeros
+    if (c < (K + 127) / 128 * 128) *reinterpret_cast<uint2*>(codes + c) = quant_codes8(v[i], q);
+  }
+  lds_barrier();
+
+  v4i acc[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) acc[i] = v4i{0, 0, 0, 0};
+  auto multiply = [&](const uint8_t* stage, int k) __attribute__((always_inline)) {
+    wait_vm<(S - 1) * L>();
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      v4i pf = {0, 0, 0, 0};
+      if (m == 0 && k < mine) pf = *reinterpret_cast<const v4i*>(codes + (s0 + k) * 128 + (kk * 4 + g) * 16);
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+        acc[i] = mma<kInt8>(read_frag<false, 16 * NC>(stage + w * kStage, i, kk, lane), pf, acc[i]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  for (int k = 0; k < mine; k += S) {
+    issue(st3, k + 3); multiply(st0, k);
+    issue(st0, k + 4); multiply(st1, k + 1);
+    issue(st1, k + 5); multiply(st2, k + 2);
+    issue(st2, k + 6); multiply(st3, k + 3);
+  }
+  stage_barrier();  // every load has landed: the first stage takes the sums
+  v4i* part = reinterpret_cast<v4i*>(st0);
+#pragma unroll
+  for (int i = 0; i < NC; ++i) part[(w * NC + i) * 64 + lane] = acc[i];
+  __syncthreads();
+  if (w < NC && m == 0) {  // fragment w: lane l holds columns 4 (l / 16) + 0..3 of row l % 16
+    v4i sum = part[w * 64 + lane];
+#pragma unroll
+    for (int u = 1; u < kFewWaves; ++u) sum += part[(u * NC + w) * 64 + lane];
+    const int c = n0 + w * 16 + 4 * g;
+    if (c < a.N) {
+      v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (token)
+        y = __builtin_convertvector(sum, v4f) * q.scale * *reinterpret_cast<const v4f*>(a.qs + long(pl.e) * a.N + c);
+      store4(a.out, long(pl.row0) * a.N + c, y, a.out_ty);
+    }
+  }
+}
+
 // dw = the splits' fp32 sums added up in their order.
 __global__ __launch_bounds__(256) void k_join(const float* __restrict__ part, int splits, long n, void* out, int ty) {
   for (long i = (long(blockIdx.x) * 256 + threadIdx.x) * 4; i < n; i += long(gridDim.x) * 1024) {
@@ -723,6 +855,41 @@ static hipError_t launch_one(int op, const MmArgs& a, hipStream_t st) {
                       : op == kDgrad ? launch_bm<kDgrad, kBf16>(a, st) : launch_bm<kWgrad, kBf16>(a, st);
   return op == kFwd ? launch_bm<kFwd, kFp16>(a, st)
                     : op == kDgrad ? launch_bm<kDgrad, kFp16>(a, st) : launch_bm<kWgrad, kFp16>(a, st);
+}
+
+bool linear_is_one_launch(int R, int K) { return R <= 1 && K <= kLinMaxK; }
+
+hipError_t launch_linear_one(const MmArgs& a, int x_ty, int swiglu, hipStream_t st) {
+  // columns per workgroup as shape_of would choose them
+  int nc = 1;
+  double least = 1e300;
+  for (int c = 2; c >= 1; --c) {
+    const double cost = std::ceil(std::ceil(a.N / (16.0 * c)) / kCUs) * (16 + 16 * c);
+    if (cost < least) {
+      least = cost;
+      nc = c;
+    }
+  }
+  const long tiles = long(a.R) * ((a.N + 16 * nc - 1) / (16 * nc));
+  const unsigned grid = unsigned((tiles + 7) / 8 * 8);
+  if (!grid) return hipSuccess;
+#define MOE_LIN(XT, GLU, NC) \
+  hipLaunchKernelGGL((k_linear_one<XT, GLU, NC>), dim3(grid), dim3(kFewWaves * 64), 0, st, a)
+#define MOE_LIN_NC(XT, GLU)            \
+  do {                                 \
+    if (nc == 2) MOE_LIN(XT, GLU, 2);  \
+    else MOE_LIN(XT, GLU, 1);          \
+  } while (0)
+  if (x_ty == kBf16) {
+    if (swiglu) MOE_LIN_NC(kBf16, true);
+    else MOE_LIN_NC(kBf16, false);
+  } else {
+    if (swiglu) MOE_LIN_NC(kFp16, true);
+    else MOE_LIN_NC(kFp16, false);
+  }
+#undef MOE_LIN_NC
+#undef MOE_LIN
+  return hipGetLastError();
 }
 
 hipError_t launch_mm(int op, const MmArgs& args, hipStream_t st) {

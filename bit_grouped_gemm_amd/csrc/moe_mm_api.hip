@@ -142,8 +142,9 @@ extern "C" int moe_mm_i8(const moe_mm_cfg* cfg, const int8_t* xq, const float* x
   return product_i8(cfg, xq, xs, wq, ws, offsets, row_token, y, stream);
 }
 
-// rows of x: the tokens where rows are gathered, else the output's rows
+// codes and scales of the rows of x: the tokens where rows are gathered, else the output's rows
 static size_t linear_bytes(const moe_mm_cfg* c, int gathered) {
+  if (linear_is_one_launch(c->R, c->K)) return 0;
   const size_t rows = size_t(gathered ? c->T : c->R);
   return rows ? align256(rows * c->K) + align256(4 * rows) : 0;
 }
@@ -164,17 +165,27 @@ extern "C" int moe_linear_i8(const moe_mm_cfg* cfg, const void* x, int swiglu, c
   const int rows = row_token ? cfg->T : cfg->R;
   const bool some = cfg->R != 0, tokens = some && rows != 0;
   int rc;
-  if ((rc = null_ptrs({{x, tokens}, {wq, true}, {ws, true}, {y, some}, {work, tokens}}))) return rc;
+  if ((rc = null_ptrs({{x, tokens}, {wq, true}, {ws, true}, {y, some}}))) return rc;
+  const bool two = tokens && !linear_is_one_launch(cfg->R, cfg->K);  // launches, with scratch between them
+  if (two && !work) return MOE_ERR_NULL_ARG;
   if ((rc = check_i8(cfg, offsets, row_token, rows))) return rc;
   if ((cfg->dtype != MOE_DT_BF16 && cfg->dtype != MOE_DT_FP16) || (swiglu != 0 && swiglu != 1))
     return MOE_ERR_UNSUPPORTED;
   if ((rc = misaligned_ptrs({{x, true}, {wq, true}, {ws, true}, {offsets, true}, {row_token, true}, {y, true}, {work, true}})))
     return rc;
-  if (tokens && work_bytes < linear_bytes(cfg, row_token != nullptr)) return MOE_ERR_WORKSPACE;
+  if (two && work_bytes < linear_bytes(cfg, row_token != nullptr)) return MOE_ERR_WORKSPACE;
+  if (some && !two) {
+    MmArgs a = args_of(cfg, x, wq, offsets, y);
+    a.row_token = row_token;
+    a.qs = ws;
+    if (mm_grid(kFwd, a) >= (1L << 31)) return MOE_ERR_BAD_SHAPE;
+    if (linear_is_one_launch(cfg->R, cfg->K))
+      return hip_status(launch_linear_one(a, cfg->dtype, swiglu, static_cast<hipStream_t>(stream)));
+  }
   int8_t* codes = static_cast<int8_t*>(work);
-  float* scales = tokens ? reinterpret_cast<float*>(codes + align256(size_t(rows) * cfg->K)) : nullptr;
-  if (tokens && (rc = hip_status(launch_quant_i8(x, cfg->dtype, swiglu, rows, cfg->K, codes, scales,
-                                                 static_cast<hipStream_t>(stream)))))
+  float* scales = two ? reinterpret_cast<float*>(codes + align256(size_t(rows) * cfg->K)) : nullptr;
+  if (two && (rc = hip_status(launch_quant_i8(x, cfg->dtype, swiglu, rows, cfg->K, codes, scales,
+                                              static_cast<hipStream_t>(stream)))))
     return rc;
   return product_i8(cfg, codes, scales, wq, ws, offsets, row_token, y, stream);
 }

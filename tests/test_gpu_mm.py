@@ -409,15 +409,17 @@ def test_quant_i8_rows_that_are_not_finite():
     bad = torch.tensor([False, True, False, True, True, False], device=DEV)
     assert torch.isnan(s[bad]).all() and not q[bad].any()
     assert torch.equal(q[~bad], clean[0][~bad]) and torch.equal(s[~bad], clean[1][~bad])
-    # and their results are NaN, the others' are not
-    y = moe.moe_linear_i8(x, codes(gen(1), 64, 256), torch.ones(64, device=DEV))
-    assert torch.isnan(y[bad]).all() and torch.isfinite(y[~bad]).all()
+    # and their results are NaN, the others' are not (also where the product quantises by itself)
+    for rows in (slice(0, 6), slice(1, 2), slice(2, 3), slice(4, 5)):
+        y = moe.moe_linear_i8(x[rows].contiguous(), codes(gen(1), 64, 256), torch.ones(64, device=DEV))
+        assert torch.isnan(y[bad[rows]]).all() and torch.isfinite(y[~bad[rows]]).all()
 
 
 @pytest.mark.parametrize("swiglu", [False, True])
 @pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
-@pytest.mark.parametrize("counts,tail,N,K", [([1], 0, 64, 256), ([3, 0, 18, 1], 2, 264, 160),
-                                             ([400, 0, 700], 9, 136, 272)])
+@pytest.mark.parametrize("counts,tail,N,K", [([1], 0, 64, 256), ([1], 0, 4096, 7168), ([1], 0, 24, 8192), ([1], 0, 72, 8208),
+                                             ([0, 1, 0, 2], 1, 264, 144), ([0, 0, 1], 0, 264, 144), ([0, 0], 1, 40, 1024), ([0, 0], 3, 40, 1024),
+                                             ([3, 0, 18, 1], 2, 264, 160), ([400, 0, 700], 9, 136, 272)])
 def test_linear_i8_equals_its_two_steps(counts, tail, N, K, dtype, swiglu):
     moe = M()
     g = gen(43)
@@ -436,6 +438,16 @@ def test_linear_i8_equals_its_two_steps(counts, tail, N, K, dtype, swiglu):
     t = torch.arange(R, device=DEV).flip(0).div(2, rounding_mode="floor").to(torch.int32)
     got = moe.moe_linear_i8(x, wq, ws, o, row_token=t, swiglu=swiglu)
     assert torch.equal(got, moe.moe_mm_i8(q, s, wq, ws, o, row_token=t, out_dtype=dtype))
+    # some rows name no token
+    for bad in (-1, R):
+        t[::2] = bad
+        got = moe.moe_linear_i8(x, wq, ws, o, row_token=t, swiglu=swiglu)
+        assert torch.equal(got, moe.moe_mm_i8(q, s, wq, ws, o, row_token=t, out_dtype=dtype)) and not got[::2].any()
+    # one row of many tokens
+    t = torch.tensor([R - 1], dtype=torch.int32, device=DEV)
+    one = offs([0] * (E - 1) + [1])
+    got = moe.moe_linear_i8(x, wq, ws, one, row_token=t, swiglu=swiglu)
+    assert torch.equal(got, moe.moe_mm_i8(q, s, wq, ws, one, row_token=t, out_dtype=dtype))
     if E == 1:  # dense
         assert torch.equal(moe.moe_linear_i8(x, wq[0], ws[0], swiglu=swiglu), want)
 

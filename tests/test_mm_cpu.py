@@ -108,7 +108,9 @@ def test_linear_i8_refusals():
     size = lambda c, g=0: moe.raw_call("moe_linear_i8_workspace_size", c, g, C.byref(n))
     assert size(cfg(R=5, K=48)) == moe.MOE_OK and n.value == 256 + 256
     assert size(cfg(R=5, K=48, T=100), 1) == moe.MOE_OK and n.value == 4864 + 512
-    assert size(cfg(R=0)) == moe.MOE_OK and n.value == 0
+    for kw in (dict(R=0), dict(R=1, K=8192), dict(R=1, K=8192, T=50)):  # one row: no codes outside the kernel
+        assert size(cfg(**kw), int("T" in kw)) == moe.MOE_OK and n.value == 0, kw
+    assert size(cfg(R=1, K=8208)) == moe.MOE_OK and n.value == 8448 + 256
     assert size(None) == moe.MOE_ERR_NULL_ARG
     assert moe.raw_call("moe_linear_i8_workspace_size", cfg(), 0, None) == moe.MOE_ERR_NULL_ARG
     for c, g in ((cfg(K=24), 0), (cfg(T=-1), 1), (cfg(), 2)):
@@ -117,14 +119,14 @@ def test_linear_i8_refusals():
         "moe_linear_i8", c, x, glu, wq, ws, o, t, y, work, nb, None)
     assert call(None) == moe.MOE_ERR_NULL_ARG
     for kw in (dict(x=None), dict(wq=None), dict(ws=None), dict(y=None), dict(work=None)):
-        assert call(cfg(), **kw) == moe.MOE_ERR_NULL_ARG, kw
+        assert call(cfg(R=5), **kw) == moe.MOE_ERR_NULL_ARG, kw
     assert call(cfg(K=24)) == moe.MOE_ERR_BAD_SHAPE
     assert call(cfg(), o=None) == moe.MOE_ERR_BAD_SHAPE
     for kw in (dict(dtype=2), dict(out_dtype=4)):
         assert call(cfg(**kw)) == moe.MOE_ERR_UNSUPPORTED, kw
     assert call(cfg(), glu=2) == moe.MOE_ERR_UNSUPPORTED
     assert call(cfg(), work=FAKE + 8) == moe.MOE_ERR_MISALIGNED
-    assert call(cfg(), nb=511) == moe.MOE_ERR_WORKSPACE
+    assert call(cfg(R=5), nb=767) == moe.MOE_ERR_WORKSPACE  # 512 + 256
 
 
 def t(*shape, dtype=torch.bfloat16):
