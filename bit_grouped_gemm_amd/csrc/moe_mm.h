@@ -36,9 +36,10 @@ struct MmArgs {
 
 // Scratch of kWgrad.
 size_t wgrad_bytes(const MmArgs& a);
-// Number of workgroups of a launch (64-bit: the ABI refuses more than 2^31).
-long mm_grid(int op, const MmArgs& a);
-hipError_t launch_mm(int op, const MmArgs& a, hipStream_t st);
+// Whether a product needs more workgroups than a launch has, and its launch
+// (*too_large: nothing was enqueued for that reason).
+bool mm_too_large(int op, const MmArgs& a);
+hipError_t launch_mm(int op, const MmArgs& a, hipStream_t st, bool* too_large);
 
 // moe_linear_i8 of one row as one launch: whether it is, and the launch (a.p:
 // the 16-bit rows of type x_ty).

@@ -803,20 +803,17 @@ size_t wgrad_bytes(const MmArgs& a) {
   return s > 1 ? size_t(s) * a.E * a.N * a.K * 4 : 0;
 }
 
-long mm_grid(int op, const MmArgs& a) {
-  const TileShape s = shape_of(op, a);
+// Workgroups of a launch in the given shape (64-bit: the ABI refuses more than 2^31).
+static long grid_of(int op, const MmArgs& a, const TileShape& s) {
   const long cols = op == kFwd ? a.N : a.K, ncol = (cols + s.cols - 1) / s.cols;
-  const long rows =
-      op == kWgrad ? long(a.E) * splits_of(a) * ((a.N + s.rows - 1) / s.rows) : row_tiles(a, s.rows);
+  const long rows = op == kWgrad ? long(a.E) * a.splits * ((a.N + s.rows - 1) / s.rows) : row_tiles(a, s.rows);
   return (rows * ncol + 7) / 8 * 8;
 }
 
 #define MOE_MM(kernel, threads) hipLaunchKernelGGL((kernel), dim3(grid), dim3(threads), 0, st, a)
 
 template <int OP, int TY>
-static hipError_t launch_bm(const MmArgs& a, hipStream_t st) {
-  const unsigned grid = unsigned(mm_grid(OP, a));
-  const TileShape s = shape_of(OP, a);
+static hipError_t launch_shape(const MmArgs& a, const TileShape& s, unsigned grid, hipStream_t st) {
   if constexpr (OP == kWgrad) {
     MOE_MM((k_mm<OP, TY, 256>), kThreads);
     if (a.splits > 1) {
@@ -827,10 +824,9 @@ static hipError_t launch_bm(const MmArgs& a, hipStream_t st) {
   } else {
     if constexpr (OP == kFwd) {
       if (s.few) {
-        const int v = s.rows / 16 * 16 + s.cols / 16;
 #define MOE_FEW(NT, NC, S) \
   case NT * 16 + NC: MOE_MM((k_mm_few<TY, NC, NT, S>), kFewWaves * 64); break;
-        switch (v) {
+        switch (s.rows + s.cols / 16) {
           MOE_FEW(1, 1, 4) MOE_FEW(1, 2, 3) MOE_FEW(1, 4, 2)
           MOE_FEW(2, 1, 4) MOE_FEW(2, 2, 2) MOE_FEW(2, 4, 2)
           MOE_FEW(4, 1, 2) MOE_FEW(4, 2, 3) MOE_FEW(4, 4, 2)
@@ -847,14 +843,48 @@ static hipError_t launch_bm(const MmArgs& a, hipStream_t st) {
 }
 #undef MOE_MM
 
-static hipError_t launch_one(int op, const MmArgs& a, hipStream_t st) {
-  if (mm_grid(op, a) == 0) return hipSuccess;
-  if (a.ty == kInt8) return launch_bm<kFwd, kInt8>(a, st);
+static hipError_t launch_one(int op, const MmArgs& a, const TileShape& s, long grid, hipStream_t st) {
+  if (grid == 0) return hipSuccess;
+  const unsigned g = unsigned(grid);
+  if (a.ty == kInt8) return launch_shape<kFwd, kInt8>(a, s, g, st);
   if (a.ty == kBf16)
-    return op == kFwd ? launch_bm<kFwd, kBf16>(a, st)
-                      : op == kDgrad ? launch_bm<kDgrad, kBf16>(a, st) : launch_bm<kWgrad, kBf16>(a, st);
-  return op == kFwd ? launch_bm<kFwd, kFp16>(a, st)
-                    : op == kDgrad ? launch_bm<kDgrad, kFp16>(a, st) : launch_bm<kWgrad, kFp16>(a, st);
+    return op == kFwd ? launch_shape<kFwd, kBf16>(a, s, g, st)
+                      : op == kDgrad ? launch_shape<kDgrad, kBf16>(a, s, g, st) : launch_shape<kWgrad, kBf16>(a, s, g, st);
+  return op == kFwd ? launch_shape<kFwd, kFp16>(a, s, g, st)
+                    : op == kDgrad ? launch_shape<kDgrad, kFp16>(a, s, g, st) : launch_shape<kWgrad, kFp16>(a, s, g, st);
+}
+
+constexpr long kMaxGrid = (1L << 31) - 1;
+
+bool mm_too_large(int op, const MmArgs& args) {
+  MmArgs a = args;
+  a.splits = op == kWgrad ? splits_of(a) : 1;
+  return grid_of(op, a, shape_of(op, a)) > kMaxGrid;
+}
+
+hipError_t launch_mm(int op, const MmArgs& args, hipStream_t st, bool* too_large) {
+  MmArgs a = args;
+  a.splits = op == kWgrad ? splits_of(a) : 1;
+  const TileShape s = shape_of(op, a);
+  const long grid = grid_of(op, a, s);
+  *too_large = grid > kMaxGrid;
+  if (*too_large) return hipSuccess;
+  const int rows = first_rows(op, a);
+  if (rows == a.R) return launch_one(op, a, s, grid, st);
+  MmArgs head = a, tail = a;
+  const long el = a.ty == kInt8 ? 1 : 2, out_el = a.out_ty == kFp32 ? 4 : 2;
+  head.R = rows;
+  tail.R = a.R - rows;
+  tail.out = static_cast<uint8_t*>(a.out) + long(rows) * a.N * out_el;
+  if (a.row_token) {
+    tail.row_token = a.row_token + rows;
+  } else {
+    tail.p = static_cast<const uint8_t*>(a.p) + long(rows) * a.K * el;
+    if (a.ps) tail.ps = a.ps + rows;
+  }
+  const TileShape hs = shape_of(op, head), ts = shape_of(op, tail);
+  const hipError_t e = launch_one(op, head, hs, grid_of(op, head, hs), st);
+  return e != hipSuccess ? e : launch_one(op, tail, ts, grid_of(op, tail, ts), st);
 }
 
 bool linear_is_one_launch(int R, int K) { return R <= 1 && K <= kLinMaxK; }
@@ -890,26 +920,6 @@ hipError_t launch_linear_one(const MmArgs& a, int x_ty, int swiglu, hipStream_t 
 #undef MOE_LIN_NC
 #undef MOE_LIN
   return hipGetLastError();
-}
-
-hipError_t launch_mm(int op, const MmArgs& args, hipStream_t st) {
-  MmArgs a = args;
-  a.splits = op == kWgrad ? splits_of(a) : 1;
-  const int rows = first_rows(op, a);
-  if (rows == a.R) return launch_one(op, a, st);
-  MmArgs head = a, tail = a;
-  const long el = a.ty == kInt8 ? 1 : 2, out_el = a.out_ty == kFp32 ? 4 : 2;
-  head.R = rows;
-  tail.R = a.R - rows;
-  tail.out = static_cast<uint8_t*>(a.out) + long(rows) * a.N * out_el;
-  if (a.row_token) {
-    tail.row_token = a.row_token + rows;
-  } else {
-    tail.p = static_cast<const uint8_t*>(a.p) + long(rows) * a.K * el;
-    if (a.ps) tail.ps = a.ps + rows;
-  }
-  const hipError_t e = launch_one(op, head, st);
-  return e != hipSuccess ? e : launch_one(op, tail, st);
 }
 
 }  // namespace moe

@@ -65,8 +65,9 @@ MmArgs args_of(const moe_mm_cfg* c, const void* p, const void* q, const int32_t*
 }
 
 int enqueue(int op, const MmArgs& a, void* stream) {
-  if (mm_grid(op, a) >= (1L << 31)) return MOE_ERR_BAD_SHAPE;
-  return hip_status(launch_mm(op, a, static_cast<hipStream_t>(stream)));
+  bool too_large = false;
+  const hipError_t e = launch_mm(op, a, static_cast<hipStream_t>(stream), &too_large);
+  return too_large ? MOE_ERR_BAD_SHAPE : hip_status(e);
 }
 
 int grouped(int op, const moe_mm_cfg* c, const void* p, const void* q, const int32_t* offsets, void* out,
@@ -120,14 +121,14 @@ extern "C" int moe_quant_i8(int R, int K, int dtype, int swiglu, const void* x, 
   return hip_status(launch_quant_i8(x, dtype, swiglu, R, K, codes, scales, static_cast<hipStream_t>(stream)));
 }
 
-static int product_i8(const moe_mm_cfg* c, const int8_t* xq, const float* xs, const int8_t* wq, const float* ws,
-                      const int32_t* offsets, const int32_t* row_token, void* y, void* stream) {
+static MmArgs args_i8(const moe_mm_cfg* c, const int8_t* xq, const float* xs, const int8_t* wq, const float* ws,
+                      const int32_t* offsets, const int32_t* row_token, void* y) {
   MmArgs a = args_of(c, xq, wq, offsets, y);
   a.ty = kInt8;
   a.row_token = row_token;
   a.ps = xs;
   a.qs = ws;
-  return enqueue(kFwd, a, stream);
+  return a;
 }
 
 extern "C" int moe_mm_i8(const moe_mm_cfg* cfg, const int8_t* xq, const float* xs, const int8_t* wq, const float* ws,
@@ -139,7 +140,7 @@ extern "C" int moe_mm_i8(const moe_mm_cfg* cfg, const int8_t* xq, const float* x
   if ((rc = check_i8(cfg, offsets, row_token, row_token ? cfg->T : cfg->R))) return rc;
   if ((rc = misaligned_ptrs({{xq, true}, {xs, true}, {wq, true}, {ws, true}, {offsets, true}, {row_token, true}, {y, true}})))
     return rc;
-  return product_i8(cfg, xq, xs, wq, ws, offsets, row_token, y, stream);
+  return enqueue(kFwd, args_i8(cfg, xq, xs, wq, ws, offsets, row_token, y), stream);
 }
 
 // codes and scales of the rows of x: the tokens where rows are gathered, else the output's rows
@@ -174,18 +175,18 @@ extern "C" int moe_linear_i8(const moe_mm_cfg* cfg, const void* x, int swiglu, c
   if ((rc = misaligned_ptrs({{x, true}, {wq, true}, {ws, true}, {offsets, true}, {row_token, true}, {y, true}, {work, true}})))
     return rc;
   if (two && work_bytes < linear_bytes(cfg, row_token != nullptr)) return MOE_ERR_WORKSPACE;
-  if (some && !two) {
+  if (some && linear_is_one_launch(cfg->R, cfg->K)) {
     MmArgs a = args_of(cfg, x, wq, offsets, y);
     a.row_token = row_token;
     a.qs = ws;
-    if (mm_grid(kFwd, a) >= (1L << 31)) return MOE_ERR_BAD_SHAPE;
-    if (linear_is_one_launch(cfg->R, cfg->K))
-      return hip_status(launch_linear_one(a, cfg->dtype, swiglu, static_cast<hipStream_t>(stream)));
+    return hip_status(launch_linear_one(a, cfg->dtype, swiglu, static_cast<hipStream_t>(stream)));
   }
   int8_t* codes = static_cast<int8_t*>(work);
   float* scales = two ? reinterpret_cast<float*>(codes + align256(size_t(rows) * cfg->K)) : nullptr;
+  const MmArgs a = args_i8(cfg, codes, scales, wq, ws, offsets, row_token, y);
+  if (mm_too_large(kFwd, a)) return MOE_ERR_BAD_SHAPE;  // before the quantiser goes out
   if (two && (rc = hip_status(launch_quant_i8(x, cfg->dtype, swiglu, rows, cfg->K, codes, scales,
                                               static_cast<hipStream_t>(stream)))))
     return rc;
-  return product_i8(cfg, codes, scales, wq, ws, offsets, row_token, y, stream);
+  return enqueue(kFwd, a, stream);
 }
