@@ -78,7 +78,7 @@ class MoeWeights(C.Structure):
 
 
 class MoeMmCfg(C.Structure):
-    _fields_ = [(n, C.c_int32) for n in ("R", "N", "K", "E", "T", "dtype", "out_dtype", "clear_tail")]
+    _fields_ = [(n, C.c_int32) for n in ("R", "N", "K", "E", "T", "dtype", "out_dtype", "clear_rest")]
 
 
 class MoeError(RuntimeError):
@@ -439,8 +439,8 @@ def _addr(name: str, t: torch.Tensor, dtypes, shape, dev: torch.device):
 
 
 def _new_or_checked(out, shape, dtype, allowed, dev):
-    """The output tensor and clear_tail: a new one has every row written, a
-    caller's keeps its rows behind the last group."""
+    """The output tensor and clear_rest: a new one has every row written, a
+    caller's keeps its rows of no group."""
     if out is not None:
         return out, 0
     if dtype not in allowed:
@@ -451,12 +451,16 @@ def _new_or_checked(out, shape, dtype, allowed, dev):
 def _matrices(w: torch.Tensor):
     if w.dim() != 3:
         raise ValueError(f"w: shape {tuple(w.shape)}, expected (E, N, K)")
+    if max(w.shape) > 0x7FFFFFFF:
+        raise ValueError(f"w: shape {tuple(w.shape)}, sizes are at most 2^31 - 1")
     return w.shape
 
 
 def _rows_of(name: str, t: torch.Tensor) -> torch.Size:
     if t.dim() != 2:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected two dimensions")
+    if t.shape[0] > 0x7FFFFFFF:
+        raise ValueError(f"{name}: {t.shape[0]} rows, at most 2^31 - 1")
     return t.shape
 
 
@@ -542,6 +546,8 @@ class _GroupedMM(torch.autograd.Function):
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
         dy = dy.contiguous()
+        if dy.data_ptr() % 16:  # a view into something else
+            dy = dy.clone()
         dx = moe_grouped_mm_dgrad(dy, w, offsets) if ctx.needs_input_grad[0] else None
         dw = moe_grouped_mm_wgrad(dy, x, offsets) if ctx.needs_input_grad[1] else None
         return dx, dw, None
@@ -554,13 +560,13 @@ def moe_grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out:
 
     x and w are both bfloat16 or both float16; offsets is int32 [E + 1] on the
     same device (moe_permute's).  The result has x's type, or float32 with
-    out_dtype=torch.float32 (the rows moe_combine takes).  Rows behind the last
-    group (r >= offsets[E]) are zeros in a new result; a caller's `out` keeps
-    what it holds there.
+    out_dtype=torch.float32 (the rows moe_combine takes).  Rows of no group (r <
+    offsets[0] or r >= offsets[E]) are zeros in a new result; a caller's `out`
+    keeps what it holds there.  All tensors are contiguous and on one GPU.
 
     Differentiable with respect to x and w (once; not with `out` or
     `out_dtype`): the gradients are moe_grouped_mm_dgrad and
-    moe_grouped_mm_wgrad, and rows behind the last group get the gradient 0."""
+    moe_grouped_mm_wgrad, and rows of no group get the gradient 0."""
     if (x.requires_grad or w.requires_grad) and torch.is_grad_enabled():
         if out is not None or out_dtype not in (None, x.dtype):
             raise ValueError("moe_grouped_mm: out and out_dtype cannot be given where a gradient is needed")
@@ -594,6 +600,8 @@ def _i8_weights(wq, ws, offsets, dev):
     if wq.dim() != (2 if offsets is None else 3):
         raise ValueError(f"wq: [N, K] without offsets, [E, N, K] with offsets; got {tuple(wq.shape)}")
     E, N, K = (1, *wq.shape) if offsets is None else wq.shape
+    if max(wq.shape) > 0x7FFFFFFF:
+        raise ValueError(f"wq: shape {tuple(wq.shape)}, sizes are at most 2^31 - 1")
     pw = _addr("wq", wq, (torch.int8,), wq.shape, dev)
     ps = _addr("ws", ws, (torch.float32,), wq.shape[:-1], dev)
     po = None if offsets is None else _addr("offsets", offsets, (torch.int32,), (E + 1,), dev)
@@ -605,6 +613,8 @@ def _row_token(row_token, T, dev):
         return T, None
     if row_token.dim() != 1:
         raise ValueError(f"row_token: shape {tuple(row_token.shape)}, expected one dimension")
+    if row_token.shape[0] > 0x7FFFFFFF:
+        raise ValueError(f"row_token: {row_token.shape[0]} rows, at most 2^31 - 1")
     return row_token.shape[0], _addr("row_token", row_token, (torch.int32,), row_token.shape, dev)
 
 
@@ -617,9 +627,8 @@ def moe_mm_i8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Te
     Dense: wq [N, K], ws [N], every row of xq.  Grouped: wq [E, N, K], ws
     [E, N] and offsets int32 [E + 1]; with row_token int32 [R] (moe_permute's)
     row r of the result takes row t = row_token[r] of xq, else t = r.
-    The result [R, N] is bfloat16 (default), float16 or float32; rows behind
-    the last group are zeros in a new result and stay as they are in a
-    caller's `out`."""
+    The result [R, N] is bfloat16 (default), float16 or float32; rows of no
+    group are zeros in a new result and stay as they are in a caller's `out`."""
     (T, width), dev = _rows_of("xq", xq), xq.device
     E, N, K, pw, pws, po = _i8_weights(wq, ws, offsets, dev)
     pq = _addr("xq", xq, (torch.int8,), (T, K), dev)

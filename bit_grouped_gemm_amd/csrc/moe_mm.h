@@ -29,7 +29,7 @@ struct MmArgs {
   int R, N, K, E, T;
   int ty;                    // operand type
   int out_ty;                // output type
-  int clear_tail;            // rows behind the last group: 1 written as zeros, 0 left alone
+  int clear_rest;            // rows of no group: 1 written as zeros, 0 left alone
   float* partial;            // kWgrad: wgrad_bytes() of scratch, or null where that is 0
   int splits;                // set by launch_mm
 };

@@ -75,15 +75,17 @@ __device__ __forceinline__ void lds_barrier() {
 
 // A group's rows and the tile's place in it.
 struct Place {
-  int e;      // group; E: the rows behind the last group (clear_tail)
+  int e;      // group; E and E + 1: the rows behind the last and before the first one (clear_rest)
   int row0;   // first row of the tile
   int rows;   // rows of the tile (<= BM)
 };
 
-// Row range of group e: the offsets clamped to [0, R], so a wrong offset
-// array reads and writes nothing outside the tensors.
+// Row range of group e (E: the rows behind the last group, E + 1: those before
+// the first): the offsets clamped to [0, R], so a wrong offset array reads and
+// writes nothing outside the tensors.
 __device__ __forceinline__ int2 group_rows(const int32_t* offsets, int e, int E, int R) {
   if (!offsets) return make_int2(e ? R : 0, R);
+  if (e > E) return make_int2(0, min(max(offsets[0], 0), R));
   const int a = min(max(offsets[e], 0), R);
   const int b = e < E ? min(max(offsets[e + 1], a), R) : R;
   return make_int2(a, b);
@@ -97,7 +99,7 @@ __device__ __forceinline__ int2 group_rows(const int32_t* offsets, int e, int E,
 // tiles before the next four.  Returns false where the id has no tile.
 __device__ __forceinline__ bool find_tile(const MmArgs& a, int BM, int ncol, int id, Place& pl, int& col) {
   const int lane = threadIdx.x & 63;
-  const int G = a.E + (a.clear_tail ? 1 : 0);
+  const int G = a.E + (a.clear_rest ? 2 : 0);
   // inclusive scan of 64 groups' tile counts, from group e0 on
   int2 r;
   int n, incl;
@@ -172,12 +174,11 @@ __device__ __forceinline__ void store4(void* out, long at, const v4f& v, int ty)
 }
 
 // The result of a sum: itself, or for int8 (sum * token's scale) * channel's
-// scales (in fp32).  Rows behind the last group, and rows that name no token,
-// have sums of zero and no scale.
+// scales (in fp32).  Rows of no group, and rows that name no token, are zeros.
 template <int TY>
 __device__ __forceinline__ v4f scaled(const MmArgs& a, int e, int row, int c, const typename Acc<TY>::type& sum) {
   if constexpr (TY == kInt8) {
-    if (e == a.E) return v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    if (e >= a.E) return v4f{0.0f, 0.0f, 0.0f, 0.0f};
     const int t = a.row_token ? a.row_token[row] : row;
     if (a.row_token && (t < 0 || t >= a.T)) return v4f{0.0f, 0.0f, 0.0f, 0.0f};
     return __builtin_convertvector(sum, v4f) * a.ps[t] * *reinterpret_cast<const v4f*>(a.qs + long(e) * a.N + c);
@@ -321,7 +322,7 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
       qs.init(we + long(ct) * kBN * ldp, long(min(kBN, a.N - ct * kBN)) * ldp, ldp, w, lane, nullptr, 0, 0);
     else
       qs.init(we + ct * kBN * 2, (long(a.N) * a.K - ct * kBN) * 2, long(a.K) * 2, w, lane, nullptr, 0, 0);
-    if (pl.e == a.E) {  // rows behind the last group: zeros
+    if (pl.e >= a.E) {  // rows of no group: zeros
       red = 0;
       qs.left = 0;
     }
@@ -479,7 +480,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_mm_few(MmArgs a) {
   if (!find_tile(a, 16 * NT, ncol, blockIdx.x, pl, ct)) return;
   const int ld = a.K * kEl;  // bytes per row of both operands
   const int n0 = ct * 16 * NC;
-  const int steps = pl.e == a.E ? 0 : (ld + 127) / 128;
+  const int steps = pl.e >= a.E ? 0 : (ld + 127) / 128;
   const int each = (steps + kFewWaves - 1) / kFewWaves;
   const int s0 = w * each, mine = max(0, min(steps - s0, each));
 
@@ -607,7 +608,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_linear_one(MmArgs a) {
   int ct;
   if (!find_tile(a, 16, ncol, blockIdx.x, pl, ct)) return;
   const int K = a.K, n0 = ct * 16 * NC;
-  const bool grouped = pl.e < a.E;  // else the row is behind the last group: zeros
+  const bool grouped = pl.e < a.E;  // else the row belongs to no group: zeros
   const int steps = grouped ? (K + 127) / 128 : 0;
   const int each = (steps + kFewWaves - 1) / kFewWaves;
   const int s0 = w * each, mine = max(0, min(steps - s0, each));
@@ -721,9 +722,9 @@ __global__ __launch_bounds__(256) void k_join(const float* __restrict__ part, in
   }
 }
 
-// Row tiles of a launch: sum over non-empty groups (and the tail) of ceil(n / rows) at most.
+// Row tiles of a launch: sum over non-empty groups (and the rows outside them) of ceil(n / rows) at most.
 long row_tiles(const MmArgs& a, int rows) {
-  const long G = (a.E < a.R ? a.E : a.R) + (a.clear_tail ? 1 : 0);
+  const long G = (a.E < a.R ? a.E : a.R) + (a.clear_rest ? 2 : 0);
   const long most = (long(a.R) + G * (rows - 1)) / rows;
   return most < a.R ? most : a.R;
 }

@@ -25,16 +25,19 @@ int null_ptrs(PtrList ps) {
     if (p.second && !p.first) return MOE_ERR_NULL_ARG;
   return MOE_OK;
 }
-int misaligned_ptrs(PtrList ps) {
-  for (auto& p : ps)
-    if (p.first && (reinterpret_cast<uintptr_t>(p.first) & 15u)) return MOE_ERR_MISALIGNED;
+// tensors on 16 bytes, index arrays (a slice of a longer one, say) on 4
+int misaligned_ptrs(std::initializer_list<const void*> tensors, std::initializer_list<const int32_t*> indices = {}) {
+  for (auto p : tensors)
+    if (reinterpret_cast<uintptr_t>(p) & 15u) return MOE_ERR_MISALIGNED;
+  for (auto p : indices)
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return MOE_ERR_MISALIGNED;
   return MOE_OK;
 }
 
 int check_dims(const moe_mm_cfg* c) {
   if (c->R < 0 || c->N < 1 || c->K < 1 || c->E < 1 || c->E > 1024) return MOE_ERR_BAD_SHAPE;
   if (c->N % 8 || c->K % 8 || c->N > kMaxDim || c->K > kMaxDim) return MOE_ERR_BAD_SHAPE;
-  if (c->clear_tail != 0 && c->clear_tail != 1) return MOE_ERR_BAD_SHAPE;
+  if (c->clear_rest != 0 && c->clear_rest != 1) return MOE_ERR_BAD_SHAPE;
   return MOE_OK;
 }
 
@@ -60,7 +63,7 @@ MmArgs args_of(const moe_mm_cfg* c, const void* p, const void* q, const int32_t*
   MmArgs a{};
   a.p = p; a.q = q; a.out = out; a.offsets = offsets;
   a.R = c->R; a.N = c->N; a.K = c->K; a.E = c->E; a.T = c->T;
-  a.ty = c->dtype; a.out_ty = c->out_dtype; a.clear_tail = c->clear_tail;
+  a.ty = c->dtype; a.out_ty = c->out_dtype; a.clear_rest = c->clear_rest;
   return a;
 }
 
@@ -77,7 +80,7 @@ int grouped(int op, const moe_mm_cfg* c, const void* p, const void* q, const int
   int rc;
   if ((rc = null_ptrs({{p, some || !p_rows}, {q, some || !q_rows}, {offsets, true}, {out, some || !out_rows}}))) return rc;
   if ((rc = check_dims(c)) || (rc = check_types(c))) return rc;
-  if ((rc = misaligned_ptrs({{p, true}, {q, true}, {offsets, true}, {out, true}, {work, true}}))) return rc;
+  if ((rc = misaligned_ptrs({p, q, out, work}, {offsets}))) return rc;
   MmArgs a = args_of(c, p, q, offsets, out);
   const size_t need = op == kWgrad ? wgrad_bytes(a) : 0;
   if (need && !work) return MOE_ERR_NULL_ARG;
@@ -117,7 +120,7 @@ extern "C" int moe_quant_i8(int R, int K, int dtype, int swiglu, const void* x, 
   if ((rc = null_ptrs({{x, R != 0}, {codes, R != 0}, {scales, R != 0}}))) return rc;
   if (R < 0 || K < 1 || K % 16 || K > kMaxDim) return MOE_ERR_BAD_SHAPE;
   if ((dtype != MOE_DT_BF16 && dtype != MOE_DT_FP16) || (swiglu != 0 && swiglu != 1)) return MOE_ERR_UNSUPPORTED;
-  if ((rc = misaligned_ptrs({{x, true}, {codes, true}, {scales, true}}))) return rc;
+  if ((rc = misaligned_ptrs({x, codes, scales}))) return rc;
   return hip_status(launch_quant_i8(x, dtype, swiglu, R, K, codes, scales, static_cast<hipStream_t>(stream)));
 }
 
@@ -138,7 +141,7 @@ extern "C" int moe_mm_i8(const moe_mm_cfg* cfg, const int8_t* xq, const float* x
   int rc;
   if ((rc = null_ptrs({{xq, tokens}, {xs, tokens}, {wq, true}, {ws, true}, {y, some}}))) return rc;
   if ((rc = check_i8(cfg, offsets, row_token, row_token ? cfg->T : cfg->R))) return rc;
-  if ((rc = misaligned_ptrs({{xq, true}, {xs, true}, {wq, true}, {ws, true}, {offsets, true}, {row_token, true}, {y, true}})))
+  if ((rc = misaligned_ptrs({xq, xs, wq, ws, y}, {offsets, row_token})))
     return rc;
   return enqueue(kFwd, args_i8(cfg, xq, xs, wq, ws, offsets, row_token, y), stream);
 }
@@ -172,7 +175,7 @@ extern "C" int moe_linear_i8(const moe_mm_cfg* cfg, const void* x, int swiglu, c
   if ((rc = check_i8(cfg, offsets, row_token, rows))) return rc;
   if ((cfg->dtype != MOE_DT_BF16 && cfg->dtype != MOE_DT_FP16) || (swiglu != 0 && swiglu != 1))
     return MOE_ERR_UNSUPPORTED;
-  if ((rc = misaligned_ptrs({{x, true}, {wq, true}, {ws, true}, {offsets, true}, {row_token, true}, {y, true}, {work, true}})))
+  if ((rc = misaligned_ptrs({x, wq, ws, y, work}, {offsets, row_token})))
     return rc;
   if (two && work_bytes < linear_bytes(cfg, row_token != nullptr)) return MOE_ERR_WORKSPACE;
   if (some && linear_is_one_launch(cfg->R, cfg->K)) {

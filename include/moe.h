@@ -330,19 +330,21 @@ int moe_prepack_weights(const moe_cfg* cfg, const moe_weights* canonical, moe_we
  * with a per-token scale, int8 weights with a per-channel scale), grouped by
  * expert or dense.
  *
- * Groups: rows offsets[e] .. offsets[e + 1] - 1 belong to group e, with
- * offsets[0] = 0 and offsets not decreasing (moe_permute's offsets of a cfg
- * without a shared expert).  Groups may be empty.  Rows from offsets[E] to R
- * belong to none: a product with clear_tail = 1 writes zeros to them, with
- * clear_tail = 0 it leaves them as they were.  Offsets are read on the device
- * and clamped to [0, R]: a wrong array gives wrong results, never an access
- * outside the tensors.
+ * Groups: rows offsets[e] .. offsets[e + 1] - 1 belong to group e; offsets do
+ * not decrease (moe_permute's offsets of a cfg without a shared expert, or a
+ * run of E + 1 of them with the matrices they belong to).  Groups may be
+ * empty.  Rows before offsets[0] and from offsets[E] on belong to none: a
+ * product with clear_rest = 1 writes zeros to them, with clear_rest = 0 it
+ * leaves them as they were.  Offsets are read on the device and clamped to [0,
+ * R]: a wrong array gives wrong results, never an access outside the tensors.
+ * Index arrays (offsets, row_token) need 4-byte alignment only.  An output
+ * overlaps no operand.
  *
  * moe_mm_cfg (host struct):
  *   R rows, N outputs and K inputs of a weight matrix, E groups (1 .. 1024),
  *   T tokens (only with row_token), dtype of the 16-bit operands
  *   (MOE_DT_BF16 / MOE_DT_FP16), out_dtype (that type or MOE_DT_FP32),
- *   clear_tail as above.
+ *   clear_rest as above.
  * Limits: N and K multiples of 8 up to 2^20 (int8: K a multiple of 16 up to
  *   2^16, which keeps every sum inside an int32), MOE_ERR_BAD_SHAPE
  *   otherwise.  R * K and R * N may pass 2^32.
@@ -354,17 +356,17 @@ typedef struct moe_mm_cfg {
   int32_t R, N, K, E, T;
   int32_t dtype;
   int32_t out_dtype;
-  int32_t clear_tail;
+  int32_t clear_rest;
 } moe_mm_cfg;
 
 /* y[r][n] = sum_k x[r][k] * w[e][n][k] for the rows r of each group e.
  *   x [R][K], w [E][N][K] of dtype; offsets int32 [E + 1]; y [R][N] of
- *   out_dtype (distinct from x).  x and y may be NULL for R = 0. */
+ *   out_dtype.  x and y may be NULL for R = 0. */
 int moe_grouped_mm(const moe_mm_cfg* cfg, const void* x, const void* w, const int32_t* offsets, void* y,
                    void* stream);
 
 /* The gradient with respect to x: dx[r][k] = sum_n dy[r][n] * w[e][n][k].
- *   dy [R][N], w [E][N][K] of dtype; dx [R][K] of out_dtype.  clear_tail = 1
+ *   dy [R][N], w [E][N][K] of dtype; dx [R][K] of out_dtype.  clear_rest = 1
  *   gives rows of no group the gradient 0. */
 int moe_grouped_mm_dgrad(const moe_mm_cfg* cfg, const void* dy, const void* w, const int32_t* offsets, void* dx,
                          void* stream);

@@ -196,6 +196,30 @@ def test_no_rows():
     assert moe.moe_linear_i8(rand(gen(1), 4, 64), wq, ws, o, row_token=t).shape == (0, 32)
 
 
+@pytest.mark.parametrize("counts", [[5, 3, 6, 2], [130, 70, 150, 60], [600, 500, 700, 40]], ids=["small", "middle", "large"])
+def test_a_run_of_the_groups(counts):
+    """Some of the experts with their slice of the offsets: rows of the others, before and behind, belong to none."""
+    moe = M()
+    g = gen(9)
+    N, K = 72, 112
+    o, R = offs(counts), sum(counts) + 7
+    x, w, dy = rand(g, R, K), rand(g, 4, N, K), rand(g, R, N)
+    a, b = int(o[1]), int(o[3])
+    part, wp = o[1:4], w[1:3].contiguous()
+    for full, some, out in ((moe.moe_grouped_mm(x, w, o), lambda **k: moe.moe_grouped_mm(x, wp, part, **k), N),
+                            (moe.moe_grouped_mm_dgrad(dy, w, o), lambda **k: moe.moe_grouped_mm_dgrad(dy, wp, part, **k), K)):
+        got = some()
+        assert torch.equal(got[a:b], full[a:b]) and not got[:a].any() and not got[b:].any()
+        keep = torch.full((R, out), 7.0, dtype=BF16, device=DEV)
+        some(out=keep)
+        assert torch.equal(keep[a:b], full[a:b]) and (keep[:a] == 7).all() and (keep[b:] == 7).all()
+    assert torch.equal(moe.moe_grouped_mm_wgrad(dy, x, part), moe.moe_grouped_mm_wgrad(dy, x, o)[1:3])
+    wq, ws = codes(g, 4, N, K), torch.rand(4, N, device=DEV, generator=g)
+    full = moe.moe_linear_i8(x, wq, ws, o)
+    got = moe.moe_linear_i8(x, wq[1:3].contiguous(), ws[1:3].contiguous(), part)
+    assert torch.equal(got[a:b], full[a:b]) and not got[:a].any() and not got[b:].any()
+
+
 def test_wrong_offsets_stay_inside_the_tensors():
     """Offsets are clamped to the rows: rows that a wrong array does name come out right, nothing else is touched."""
     moe = M()
@@ -233,6 +257,22 @@ def test_rows_past_32_bits():
     near(dw, ref, mag, 300, "dw")
 
 
+def test_int8_rows_past_32_bits():
+    """R * K past 2^31 codes, and past 2^32 bytes of activations."""
+    moe = M()
+    g = gen(14)
+    R, K, N = (1 << 18) + 21, 8704, 72
+    x = torch.zeros(R, K, dtype=BF16, device=DEV)
+    x[-70:] = rand(g, 70, K)
+    q, s = moe.moe_quant_i8(x)
+    want = moe.moe_quant_i8(x[-70:].contiguous())
+    assert torch.equal(q[-70:], want[0]) and torch.equal(s[-70:], want[1]) and not q[:-70].any()
+    wq, ws = codes(g, N, K), torch.rand(N, device=DEV, generator=g) * 1e-3
+    y = moe.moe_mm_i8(q, s, wq, ws, out_dtype=FP32)
+    near_i8(y[-70:], (want[0].double() @ wq.double().t()) * want[1].double()[:, None] * ws.double(), "last rows")
+    assert not y[:-70].any()
+
+
 # ------------------------------------------------------------------ autograd
 @pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
 def test_autograd_equals_the_gradient_products(dtype):
@@ -252,6 +292,10 @@ def test_autograd_equals_the_gradient_products(dtype):
     x2 = x.detach().clone().requires_grad_()
     moe.moe_grouped_mm(x2, w.detach(), o).sum().backward()
     assert torch.equal(x2.grad, moe.moe_grouped_mm_dgrad(torch.ones_like(y), w.detach(), o))
+    # a gradient that is a view at an odd place
+    x3 = x.detach().clone().requires_grad_()
+    flat = torch.empty(y.numel() + 4, dtype=dtype, device=DEV)[4:].view_as(y).copy_(dy)
+    assert torch.equal(torch.autograd.grad(moe.moe_grouped_mm(x3, w.detach(), o), x3, flat)[0], x.grad)
     # the weights used twice: their gradients add up
     w2 = w.detach().clone().requires_grad_()
     (moe.moe_grouped_mm(x.detach(), w2, o) + moe.moe_grouped_mm(x.detach(), w2, o)).backward(dy)
@@ -486,6 +530,38 @@ def test_on_another_stream_and_replayed():
         torch.cuda.synchronize()
         got = [h.clone() for h in held]
         assert all(torch.equal(a, b) for a, b in zip(got, run())), counts
+
+
+def test_a_training_step_in_a_graph():
+    """Forward and backward captured together, replayed with new values and other groups."""
+    moe = M()
+    g = gen(61)
+    R, N, K = 150, 72, 128
+    x, w = rand(g, R, K).requires_grad_(), rand(g, 3, N, K).requires_grad_()
+    dy, o = rand(g, R, N), offs([50, 0, 90])
+
+    def step():
+        y = moe.moe_grouped_mm(x, w, o)
+        return (y.detach(), *torch.autograd.grad(y, (x, w), dy))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for i, counts in enumerate(([50, 0, 90], [1, 149, 0], [0, 0, 3])):
+        with torch.no_grad():
+            x.copy_(rand(gen(300 + i), R, K))
+        o.copy_(offs(counts))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [h.clone() for h in held]
+        xd, wd = x.detach(), w.detach()
+        want = (moe.moe_grouped_mm(xd, wd, o), moe.moe_grouped_mm_dgrad(dy, wd, o), moe.moe_grouped_mm_wgrad(dy, xd, o))
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), counts
 
 
 # ------------------------------------------------------------------ together

@@ -20,7 +20,7 @@ def lib():
 
 
 def cfg(**kw):
-    base = dict(R=4, N=64, K=64, E=2, T=4, dtype=0, out_dtype=0, clear_tail=0)
+    base = dict(R=4, N=64, K=64, E=2, T=4, dtype=0, out_dtype=0, clear_rest=0)
     base.update(kw)
     return C.byref(moe.MoeMmCfg(*[base[n] for n, _ in moe.MoeMmCfg._fields_]))
 
@@ -38,12 +38,12 @@ def test_grouped_refusals(name):
     # NULL comes before the shape
     assert call(cfg(N=7), p=None) == moe.MOE_ERR_NULL_ARG
     for kw in (dict(R=-1), dict(N=0), dict(K=0), dict(E=0), dict(E=1025), dict(N=60), dict(K=12), dict(N=(1 << 20) + 8),
-               dict(K=(1 << 20) + 8), dict(clear_tail=2)):
+               dict(K=(1 << 20) + 8), dict(clear_rest=2)):
         assert call(cfg(**kw)) == moe.MOE_ERR_BAD_SHAPE, kw
     for kw in (dict(dtype=2, out_dtype=2), dict(dtype=3), dict(out_dtype=1), dict(dtype=1, out_dtype=0),
                dict(out_dtype=-1)):
         assert call(cfg(**kw)) == moe.MOE_ERR_UNSUPPORTED, kw
-    for kw in (dict(p=FAKE + 8), dict(q=FAKE + 2), dict(o=FAKE + 4), dict(out=FAKE + 8)):
+    for kw in (dict(p=FAKE + 8), dict(q=FAKE + 2), dict(o=FAKE + 2), dict(out=FAKE + 8)):
         assert call(cfg(), **kw) == moe.MOE_ERR_MISALIGNED, kw
 
 
@@ -98,8 +98,8 @@ def test_mm_i8_refusals():
     assert call(cfg(T=1 << 25), t=FAKE) == moe.MOE_ERR_BAD_SHAPE      # T * K reaches 2^31
     for kw in (dict(out_dtype=3), dict(out_dtype=-1)):
         assert call(cfg(**kw)) == moe.MOE_ERR_UNSUPPORTED, kw
-    for kw in (dict(xq=FAKE + 8), dict(xs=FAKE + 4), dict(wq=FAKE + 8), dict(ws=FAKE + 4), dict(o=FAKE + 4),
-               dict(t=FAKE + 4), dict(y=FAKE + 8)):
+    for kw in (dict(xq=FAKE + 8), dict(xs=FAKE + 4), dict(wq=FAKE + 8), dict(ws=FAKE + 4), dict(o=FAKE + 2),
+               dict(t=FAKE + 1), dict(y=FAKE + 8)):
         assert call(cfg(), **kw) == moe.MOE_ERR_MISALIGNED, kw
 
 
@@ -163,6 +163,8 @@ def test_python_refusals():
                               t(32, dtype=torch.float32), out_dtype=torch.float64),
         lambda: moe.moe_linear_i8(x, w[0, :, :48].contiguous().to(torch.int8), t(32, dtype=torch.float32)),
         lambda: moe.moe_linear_i8(x, w[0].to(torch.int8), t(32, dtype=torch.float32), swiglu=True),
+        lambda: moe.moe_grouped_mm(t(1, 8).expand(1 << 31, 8), w, off),             # more rows than an int32 counts
+        lambda: moe.moe_quant_i8(t(1, 16).expand(1 << 32, 16)),
         # tensors that are no GPU's are refused, not computed elsewhere
         lambda: moe.moe_grouped_mm(x, w, off),
         lambda: moe.moe_quant_i8(x),
