@@ -63,6 +63,18 @@ __device__ __forceinline__ void stage_barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// The same, but for this wave's last N loads.
+template <int N>
+__device__ __forceinline__ void stage_barrier_but() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // Barrier after this wave's LDS accesses; loads stay in flight.
 __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_sched_barrier(0);
@@ -95,8 +107,10 @@ __device__ __forceinline__ int2 group_rows(const int32_t* offsets, int e, int E,
 // at a time), so nothing has to be prepared on the host.  `id` runs over this
 // launch's workgroups; workgroup ids are dealt round-robin over the 8 XCDs,
 // and XCD x takes tiles [x per, (x + 1) per): neighbouring tiles, which share
-// rows or weights, share an L2.  Tiles run over all columns of four row
-// tiles before the next four.  Returns false where the id has no tile.
+// rows or weights, share an L2.  Tiles run over all columns of four row tiles
+// before the next four, of eight where there are eight columns or more
+// (measured with 6, 8 and 16 columns: 4 and 8 are within 2 % of the best of 2,
+// 4, 8 and 16).  Returns false where the id has no tile.
 __device__ __forceinline__ bool find_tile(const MmArgs& a, int BM, int ncol, int id, Place& pl, int& col) {
   const int lane = threadIdx.x & 63;
   const int G = a.E + (a.clear_rest ? 2 : 0);
@@ -126,10 +140,11 @@ __device__ __forceinline__ bool find_tile(const MmArgs& a, int BM, int ncol, int
   const uint32_t tiles = uint32_t(total) * uint32_t(ncol), per = (tiles + 7) / 8;
   const uint32_t t = (id & 7) * per + (id >> 3);
   if (uint32_t(id >> 3) >= per || t >= tiles) return false;
-  const uint32_t block = t / (4u * ncol), in = t - block * 4u * ncol;
-  const uint32_t wide = min(4u, uint32_t(total) - block * 4u);  // row tiles of this block of columns
+  const uint32_t high = ncol < 8 ? 4 : 8;
+  const uint32_t block = t / (high * ncol), in = t - block * high * ncol;
+  const uint32_t wide = min(high, uint32_t(total) - block * high);  // row tiles of this block of columns
   col = int(in / wide);
-  const int want = int(block * 4u + in % wide);
+  const int want = int(block * high + in % wide);
   int before = 0;
   for (int e0 = 0; e0 < G; e0 += 64) {
     if (G > 64) scan(e0);  // else as it stands
@@ -270,12 +285,20 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
   constexpr int kStep = 128 / kEl;  // reduction length of a step
   using PS = Stream<PT, BM>;
   using QS = Stream<QT, kBN>;
+  // Stages: as many as the CU's LDS holds (two workgroups of BM = 64 share it).
+  // Each is needed a step later than its loads go out, so a third one gives
+  // loads that miss the L2 two steps' time.  (Ragged groups, 32768 rows, 4096
+  // -> 1536, E=64: two stages of both 482 us, a third of q 435; 2048 -> 1408:
+  // dx 157 against 133; nothing where all is in the L2.)
+  constexpr int NP = BM == 128 ? 3 : 2, NQ = BM == 64 ? 2 : 3;
   // one array per stage: the compiler's alias analysis then keeps a stage's
   // reads free of waits for the other stage's loads
   __shared__ __align__(1024) uint8_t p0[PS::kBytes];
   __shared__ __align__(1024) uint8_t p1[PS::kBytes];
+  __shared__ __align__(1024) uint8_t p2[NP > 2 ? PS::kBytes : 16];
   __shared__ __align__(1024) uint8_t q0[QS::kBytes];
   __shared__ __align__(1024) uint8_t q1[QS::kBytes];
+  __shared__ __align__(1024) uint8_t q2[NQ > 2 ? QS::kBytes : 16];
 
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = w >> 2, wn = w & 3;
@@ -335,13 +358,16 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
 #pragma unroll
     for (int j = 0; j < NF; ++j) acc[i][j] = typename Acc<TY>::type{0, 0, 0, 0};
 
-  int kleft = red * kEl;  // bytes of a C row from this step on
-  auto issue = [&](uint8_t* sp, uint8_t* sq) __attribute__((always_inline)) {
-    ps.issue(sp, w, kleft);
-    qs.issue(sq, w, kleft);
+  int kleft_p = red * kEl, kleft_q = kleft_p;  // bytes of a C row from the next step to load on
+  auto issue_p = [&](uint8_t* sp) __attribute__((always_inline)) {
+    ps.issue(sp, w, kleft_p);
     ps.advance();
+    kleft_p -= 128;
+  };
+  auto issue_q = [&](uint8_t* sq) __attribute__((always_inline)) {
+    qs.issue(sq, w, kleft_q);
     qs.advance();
-    kleft -= 128;
+    kleft_q -= 128;
   };
   // The fragments of half a step.  Each half is read while the half before it
   // is multiplied, so a step has one barrier, between its halves: by then every
@@ -363,13 +389,14 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
       for (int j = 0; j < NF; ++j) acc[i][j] = mma<TY>(f.q[j], f.p[i], acc[i][j]);
   };
   Half even, odd;
-  // one step from stage x, with y the other stage (what is read from it after
+  // one step from stage x, with y the next stage (what is read from it after
   // the last step goes unused)
   auto step = [&](uint8_t* px, uint8_t* qx, const uint8_t* py, const uint8_t* qy) __attribute__((always_inline)) {
     read(odd, px, qx, 1);
     multiply(even);
-    stage_barrier();
-    issue(px, qx);
+    stage_barrier_but<(NP - 2) * PS::kLoads + (NQ - 2) * QS::kLoads>();  // the next stage has arrived
+    issue_p(px);
+    issue_q(qx);
     read(even, py, qy, 0);
     multiply(odd);
 #pragma unroll
@@ -379,16 +406,58 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
       __builtin_amdgcn_sched_group_barrier(0x008, MF * NF / 8, 0);
     }
   };
-  issue(p0, q0);
-  stage_barrier();
-  issue(p1, q1);
+  // in the order of the steps: p(s), q(s + NQ - 2), p(s + 1), ... (see step)
+  issue_p(p0);
+  issue_q(q0);
+  if constexpr (NQ > NP) issue_q(q1);
+  issue_p(p1);
+  issue_q(NQ > NP ? q2 : q1);
+  if constexpr (NP > 2) {
+    issue_p(p2);
+    issue_q(q2);
+  }
+  stage_barrier_but<(NP - 1) * PS::kLoads + (NQ - 1) * QS::kLoads>();
   read(even, p0, q0, 0);
   int s = 0;
-  for (; s + 1 < steps; s += 2) {
-    step(p0, q0, p1, q1);
-    step(p1, q1, p0, q0);
+  if constexpr (NQ == 2) {
+    for (; s + 1 < steps; s += 2) {
+      step(p0, q0, p1, q1);
+      step(p1, q1, p0, q0);
+    }
+    if (s < steps) step(p0, q0, p1, q1);
+  } else if constexpr (NP == 3) {
+    for (; s + 2 < steps; s += 3) {
+      step(p0, q0, p1, q1);
+      step(p1, q1, p2, q2);
+      step(p2, q2, p0, q0);
+    }
+    if (s < steps) {
+      step(p0, q0, p1, q1);
+      if (s + 1 < steps) step(p1, q1, p2, q2);
+    }
+  } else {
+    for (; s + 5 < steps; s += 6) {
+      step(p0, q0, p1, q1);
+      step(p1, q1, p0, q2);
+      step(p0, q2, p1, q0);
+      step(p1, q0, p0, q1);
+      step(p0, q1, p1, q2);
+      step(p1, q2, p0, q0);
+    }
+    if (s < steps) {
+      step(p0, q0, p1, q1);
+      if (s + 1 < steps) {
+        step(p1, q1, p0, q2);
+        if (s + 2 < steps) {
+          step(p0, q2, p1, q0);
+          if (s + 3 < steps) {
+            step(p1, q0, p0, q1);
+            if (s + 4 < steps) step(p0, q1, p1, q2);
+          }
+        }
+      }
+    }
   }
-  if (s < steps) step(p0, q0, p1, q1);
 
   // Lane l holds columns 4 (l / 16) + 0..3 of row l % 16 of each fragment.
   // Sixteen rows at a time go through a piece of LDS of the wave's own, so that
