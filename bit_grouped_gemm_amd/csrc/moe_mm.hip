@@ -7,7 +7,7 @@
 // x, w forward, dy in kDgrad) or "T" (k is the row index: w in kDgrad, both
 // operands of kWgrad).  A K step is 128 bytes of every C row (64 16-bit or
 // 128 int8 values) or 64 rows of a T operand, brought by direct-to-LDS
-// loads into one of two stages while the other is multiplied.
+// loads into one stage of a ring while another is multiplied.
 //   C stage: rows of 128 bytes, 16-byte chunk c of row r at slot c ^ (r & 7),
 //     so that the 16 lanes that read one chunk of 16 rows for the MFMA spread
 //     over the banks while a load still covers whole 128-byte lines.
@@ -18,6 +18,13 @@
 // Rows, columns and K steps past an operand's end read zeros through the
 // buffer descriptor's bounds check, which ends at the group's last row, so a
 // NaN of another group never meets this one's zeros.
+//
+// Large products are bound by the loads' way into LDS together with the power
+// that the matrix units draw: one 4096 x 4096 x 7168 bf16 product takes 167 us
+// (1440 TFLOP/s; the library's 152 to 165 us on the same card), 57 % of the
+// cycles in MFMAs at 2.04 GHz; without loads 155 us, without MFMAs 122, and on
+// zeros, which draw less, 156.  Ragged groups of cold weights wait for HBM on
+// top of it (E=64, 32768 rows, 4096 -> 1536: 440 us, 936 TFLOP/s).
 #include <cmath>
 
 #include "moe_device.h"
@@ -525,7 +532,10 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
 // a ring of S stages of its own, so nothing waits for another wave until the
 // sums are added up, in the order of the waves, through LDS.  Bound by the
 // weights' bytes and their latency: S - 1 steps of 2 KB per 16 columns are in
-// flight per wave, on every CU.
+// flight per wave, on every CU.  S is what lets two workgroups share a CU where
+// that pays (16 x 64 tiles: S = 2 and two of them 131 us, S = 4 and one 177; 61
+// tokens, top-8 of 64, 1536 -> 4096).  One bf16 token through 8 of 64 experts,
+// 4096 -> 1536: 18 us, 5.6 TB/s of weights; a copy reaches 4.8 TB/s on this card.
 constexpr int kFewWaves = 4;
 
 template <int TY, int NC, int NT, int S>
@@ -805,14 +815,14 @@ struct TileShape {
 
 // The tile shape whose launch brings the fewest bytes through a CU: rounds of
 // one tile per CU times (rows + columns) of a tile.  Times follow that count
-// over the whole range where tiles do not yet fill the chip (H = K = 4096
-// bf16, one matrix: 3 us + 0.165 us per row or column; R=64, N=4096: 16 x 64
-// 14.3 us, 32 x 32 12.6, 64 x 64 22.1, 64 x 256 58; R=1024: 32 x 32 146, 64 x
-// 64 84, 256 x 256 101), and from there on it prefers the large tiles, which
-// the matrix units need.  The row tiles of ragged groups are estimated: groups
-// with a row, each half a tile more than its mean needs.  Among equals the
-// first, so the smaller tiles and k_mm_few (H=4096 to I=1536, 8 tokens
-// top-8 of 64: 94 us against 123).
+// where tiles do not yet fill the chip (one bf16 matrix, K = N = 4096, us: 64
+// rows in tiles of 16 x 64 14.9, 32 x 32 13.9, 64 x 64 22.0, 64 x 256 59; 1024
+// rows in 32 x 32 125, 64 x 64 79, 64 x 256 64, 256 x 256 76), and from there on it
+// prefers the large tiles, which the matrix units need (E=64, 4096 -> 1536:
+// 6144 rows in 64 x 256 222, 128 x 256 175, 256 x 256 198; 32768 rows 633, 470,
+// 440).  The row tiles of ragged groups are estimated: groups with a row, each
+// half a tile more than its mean needs.  Among equals the first, so the smaller
+// tiles and k_mm_few (8 tokens, top-8 of 64: 94 us against 125).
 TileShape shape_of(int op, const MmArgs& a, double* cost_of = nullptr) {
   if (op == kWgrad) return {0, 256, kBN};
   static const TileShape shapes[] = {{1, 16, 64}, {1, 16, 32}, {1, 16, 16}, {1, 32, 32}, {1, 32, 64}, {1, 32, 16},

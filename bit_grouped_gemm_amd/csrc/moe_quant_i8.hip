@@ -4,7 +4,7 @@
 // One pass over the data: a row's values stay in registers between the
 // maximum and the rounding (rows of up to 16384 values; longer ones are read
 // again, from L2 as a rule).  Bound by HBM: 2 (SwiGLU: 4) bytes in and one out
-// per value.
+// per value; 32768 rows of 7168: 127 us, 5.5 TB/s.
 #include "moe_quant_i8.h"
 
 namespace moe {
@@ -64,7 +64,9 @@ hipError_t launch_ty(const uint16_t* x, int R, int K, int8_t* codes, float* scal
 #define MOE_QUANT(TH, NC)                                                                                       \
   hipLaunchKernelGGL((k_quant_i8<TY, GLU, TH, NC>), dim3((long(R) * TH + 255) / 256), dim3(256), 0, st, x, R, K, \
                      codes, scales)
-  // a wave per row while its lanes hold the row in two chunks each
+  // a wave per row up to 1024 values, a workgroup from there on (32768 rows:
+  // K = 1024 17.4 us against 25.5, K = 2048 33.0 against 33.1, K = 4096 78
+  // against 69; 488 rows of 1536, SwiGLU: 4.4 against 3.5)
   if (K <= 512) MOE_QUANT(64, 1);
   else if (K <= 1024) MOE_QUANT(64, 2);
   else if (K <= 2048) MOE_QUANT(256, 1);
