@@ -319,13 +319,14 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
   const uint8_t* P = static_cast<const uint8_t*>(a.p);
   const uint8_t* Q = static_cast<const uint8_t*>(a.q);
   if constexpr (OP == kWgrad) {
-    // tile of group e: rows are N, columns K; XCD x takes a run of tiles.  A
+    // tile of group e: rows are N, columns K.  Groups differ in length, so every
+    // XCD takes a run of each group's tiles (all rows of a column first, which
+    // share the column's strip of x); the first XCD moves on with the group.  A
     // group's rows may be split over a.splits workgroups, in whole steps.
-    const uint32_t nrow = (a.N + BM - 1) / BM, one = nrow * ncol;
-    const uint32_t tiles = a.E * a.splits * one, per = (tiles + 7) / 8;
-    const uint32_t t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= per || t >= tiles) return;
-    const uint32_t part = t / one, in = t - part * one;
+    const uint32_t nrow = (a.N + BM - 1) / BM, one = nrow * ncol, run = (one + 7) / 8;
+    const uint32_t part = (blockIdx.x >> 3) / run;
+    const uint32_t in = ((blockIdx.x + part) & 7) * run + (blockIdx.x >> 3) - part * run;
+    if (part >= uint32_t(a.E) * a.splits || in >= one) return;
     pl.e = int(part / a.splits);
     split = int(part - pl.e * uint32_t(a.splits));
     ct = int(in / nrow);
@@ -886,8 +887,8 @@ size_t wgrad_bytes(const MmArgs& a) {
 // Workgroups of a launch in the given shape (64-bit: the ABI refuses more than 2^31).
 static long grid_of(int op, const MmArgs& a, const TileShape& s) {
   const long cols = op == kFwd ? a.N : a.K, ncol = (cols + s.cols - 1) / s.cols;
-  const long rows = op == kWgrad ? long(a.E) * a.splits * ((a.N + s.rows - 1) / s.rows) : row_tiles(a, s.rows);
-  return (rows * ncol + 7) / 8 * 8;
+  if (op == kWgrad) return ((a.N + s.rows - 1) / s.rows * ncol + 7) / 8 * 8 * a.E * a.splits;
+  return (row_tiles(a, s.rows) * ncol + 7) / 8 * 8;
 }
 
 #define MOE_MM(kernel, threads) hipLaunchKernelGGL((kernel), dim3(grid), dim3(threads), 0, st, a)
