@@ -20,11 +20,12 @@
 // NaN of another group never meets this one's zeros.
 //
 // Large products are bound by the loads' way into LDS together with the power
-// that the matrix units draw: one 4096 x 4096 x 7168 bf16 product takes 167 us
-// (1440 TFLOP/s; the library's 152 to 165 us on the same card), 57 % of the
-// cycles in MFMAs at 2.04 GHz; without loads 155 us, without MFMAs 122, and on
-// zeros, which draw less, 156.  Ragged groups of cold weights wait for HBM on
-// top of it (E=64, 32768 rows, 4096 -> 1536: 440 us, 936 TFLOP/s).
+// that the matrix units draw: one 4096 x 4096 x 7168 bf16 product takes 170 us
+// (1416 TFLOP/s; the library's 156 us on the same card, but dx 186 against 189
+// and dW 182 against 224), 70 % of the cycles in MFMAs at 1.9 GHz; without
+// loads 155 us, without MFMAs 122, and on zeros, which draw less, 156.  Ragged
+// groups of cold weights wait for HBM on top of it (E=64, 32768 rows, 4096 ->
+// 1536: 440 us, 936 TFLOP/s).
 #include <cmath>
 
 #include "moe_device.h"
@@ -223,7 +224,9 @@ struct Stream {
   uint32_t off[kLoads];
   int chunk;       // C: byte of the lane's chunk in the 128-byte step
 
-  // `ld`: bytes per memory row.  rows: C: valid rows of the tile.
+  // `b`: the first byte; `bytes` may be read from there on; `ld`: bytes per memory
+  // row.  `index` (C): the memory row of each of the tile's nindex rows, counted
+  // from b; one outside [0, nrows_of_p) reads as zeros.
   __device__ __forceinline__ void init(const uint8_t* b, long bytes, long ld, int w, int lane,
                                        const int32_t* index, int nindex, int nrows_of_p) {
     base = b;
@@ -264,8 +267,8 @@ struct Stream {
   }
 };
 
-// MFMA fragment i (16 rows / columns) of a stage for this lane; kk: the half
-// of the K step; t0: the first fragment of the wave in the stage.
+// MFMA fragment `frag` (16 rows or columns) of a stage for this lane; kk: the
+// half of the K step.
 template <bool TR, int ROWS>
 __device__ __forceinline__ v4i read_frag(const uint8_t* stage, int frag, int kk, int lane) {
   const int m = lane & 15, g = lane >> 4;
@@ -366,7 +369,7 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
 #pragma unroll
     for (int j = 0; j < NF; ++j) acc[i][j] = typename Acc<TY>::type{0, 0, 0, 0};
 
-  int kleft_p = red * kEl, kleft_q = kleft_p;  // bytes of a C row from the next step to load on
+  int kleft_p = OP == kWgrad ? 0 : red * kEl, kleft_q = kleft_p;  // bytes of a C row from the next step to load on
   auto issue_p = [&](uint8_t* sp) __attribute__((always_inline)) {
     ps.issue(sp, w, kleft_p);
     ps.advance();
@@ -379,8 +382,9 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
   };
   // The fragments of half a step.  Each half is read while the half before it
   // is multiplied, so a step has one barrier, between its halves: by then every
-  // wave has read the whole stage, which the step after next may overwrite, and
-  // the next stage, whose loads went out one step earlier, has arrived.
+  // wave has read the whole stage, whose place the next loads take, and the next
+  // stage has arrived.  Loads complete in the order they went out, so it is enough
+  // to wait for all but those of the stages after that one.
   struct Half {
     v4i p[MF], q[NF];
   };
@@ -471,7 +475,7 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
   // Sixteen rows at a time go through a piece of LDS of the wave's own, so that
   // a store covers whole rows of its 64 columns (128 or 256 bytes in a line)
   // instead of 32-byte pieces, and past the caches (268 MB of bf16 gradients, 16
-  // groups of 1024 rows: 318 us, in 32-byte pieces 408, without stores 285).
+  // groups of 1024 rows: 90 us less than in pieces).
   stage_barrier();  // no stage is read or filled any more
   int el = lane;
   asm volatile("" : "+v"(el));  // addresses from here on are not formed before the loop, which has no registers for them

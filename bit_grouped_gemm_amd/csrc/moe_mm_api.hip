@@ -13,6 +13,7 @@ using namespace moe;
 namespace {
 
 constexpr int kMaxDim = 1 << 20;   // N, K: a tile's rows stay inside a 32-bit byte range
+constexpr int kMaxRows = 0x7FFFFFFF - 1023;  // a row count rounded up to a tile stays an int32
 constexpr int kMaxKInt8 = 1 << 16;  // 128 * 128 * K stays inside an int32 sum
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -35,7 +36,7 @@ int misaligned_ptrs(std::initializer_list<const void*> tensors, std::initializer
 }
 
 int check_dims(const moe_mm_cfg* c) {
-  if (c->R < 0 || c->N < 1 || c->K < 1 || c->E < 1 || c->E > 1024) return MOE_ERR_BAD_SHAPE;
+  if (c->R < 0 || c->R > kMaxRows || c->N < 1 || c->K < 1 || c->E < 1 || c->E > 1024) return MOE_ERR_BAD_SHAPE;
   if (c->N % 8 || c->K % 8 || c->N > kMaxDim || c->K > kMaxDim) return MOE_ERR_BAD_SHAPE;
   if (c->clear_rest != 0 && c->clear_rest != 1) return MOE_ERR_BAD_SHAPE;
   return MOE_OK;

@@ -104,6 +104,8 @@ SHAPES = {
     "one_large_group": ([1025], 0, 1032, 520),
     "skewed": ([900] + [0] * 30 + [1], 0, 256, 128),
     "many_groups": ([i % 5 for i in range(200)], 9, 64, 64),
+    "most_groups": ([i % 3 for i in range(1024)], 5, 16, 32),
+    "many_large_groups": ([257, 300, 0] * 45, 0, 72, 80),
     "long_k": ([2, 30], 0, 16, 8200),
     "rows_split_for_dw": ([3000, 0, 1511], 70, 72, 136),
     "rows_split_for_one_dw": ([33001], 0, 136, 264),

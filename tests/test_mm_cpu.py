@@ -37,7 +37,7 @@ def test_grouped_refusals(name):
         assert call(cfg(), **kw) == moe.MOE_ERR_NULL_ARG, kw
     # NULL comes before the shape
     assert call(cfg(N=7), p=None) == moe.MOE_ERR_NULL_ARG
-    for kw in (dict(R=-1), dict(N=0), dict(K=0), dict(E=0), dict(E=1025), dict(N=60), dict(K=12), dict(N=(1 << 20) + 8),
+    for kw in (dict(R=-1), dict(R=(1 << 31) - 1023), dict(N=0), dict(K=0), dict(E=0), dict(E=1025), dict(N=60), dict(K=12), dict(N=(1 << 20) + 8),
                dict(K=(1 << 20) + 8), dict(clear_rest=2)):
         assert call(cfg(**kw)) == moe.MOE_ERR_BAD_SHAPE, kw
     for kw in (dict(dtype=2, out_dtype=2), dict(dtype=3), dict(out_dtype=1), dict(dtype=1, out_dtype=0),
@@ -48,8 +48,8 @@ def test_grouped_refusals(name):
 
 
 def test_grouped_refuses_more_workgroups_than_a_launch_has():
-    # 2^31 - 1 rows of 2^20 outputs: the tile count passes 2^31
-    assert moe.raw_call("moe_grouped_mm", cfg(R=(1 << 31) - 1, N=1 << 20, E=1), FAKE, FAKE, FAKE, FAKE,
+    # 2^31 - 1024 rows of 2^20 outputs: the tile count passes 2^31
+    assert moe.raw_call("moe_grouped_mm", cfg(R=(1 << 31) - 1024, N=1 << 20, E=1), FAKE, FAKE, FAKE, FAKE,
                         None) == moe.MOE_ERR_BAD_SHAPE
 
 
