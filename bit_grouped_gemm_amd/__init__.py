@@ -438,14 +438,14 @@ def _addr(name: str, t: torch.Tensor, dtypes, shape, dev: torch.device):
     return _ptr(t)
 
 
-def _new_or_checked(out, shape, dtype, allowed, dev):
+def _new_or_checked(out, shape, dtype, allowed, like):
     """The output tensor and clear_rest: a new one has every row written, a
     caller's keeps its rows of no group."""
     if out is not None:
         return out, 0
     if dtype not in allowed:
         raise ValueError(f"out_dtype {dtype} is not one of {', '.join(map(str, allowed))}")
-    return torch.empty(shape, dtype=dtype, device=dev), 1
+    return like.new_empty(shape, dtype=dtype), 1
 
 
 def _matrices(w: torch.Tensor):
@@ -474,7 +474,7 @@ def _grouped(name, rows, p, w, offsets, width, other, out, out_dtype):
     po = _addr("offsets", offsets, (torch.int32,), (E + 1,), dev)
     if out is not None and out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
-    out, clear = _new_or_checked(out, (R, other), out_dtype or dt, allowed, dev)
+    out, clear = _new_or_checked(out, (R, other), out_dtype or dt, allowed, p)
     py = _addr("out", out, allowed, (R, other), dev)
     c = MoeMmCfg(R, N, K, E, 0, _DT[dt], _DT[out.dtype], clear)
     _call(name, dev.index, C.byref(c), pp, pw, po, py)
@@ -512,7 +512,7 @@ def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     po = _addr("offsets", offsets, (torch.int32,), (E + 1,), dev)
     if out is not None and out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
-    out, _ = _new_or_checked(out, (E, N, K), out_dtype or dt, allowed, dev)
+    out, _ = _new_or_checked(out, (E, N, K), out_dtype or dt, allowed, x)
     pw = _addr("out", out, allowed, (E, N, K), dev)
     c = MoeMmCfg(R, N, K, E, 0, _DT[dt], _DT[out.dtype], 0)
     if work is None:
@@ -544,12 +544,27 @@ class _GroupedMM(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
+        # moe_grouped_mm_dgrad and moe_grouped_mm_wgrad, with one round of checks
         x, w, offsets = ctx.saved_tensors
         dy = dy.contiguous()
         if dy.data_ptr() % 16:  # a view into something else
             dy = dy.clone()
-        dx = moe_grouped_mm_dgrad(dy, w, offsets) if ctx.needs_input_grad[0] else None
-        dw = moe_grouped_mm_wgrad(dy, x, offsets) if ctx.needs_input_grad[1] else None
+        (E, N, K), R, dt, dev = w.shape, x.shape[0], x.dtype, x.device
+        pd = _addr("dy", dy, (dt,), (R, N), dev)
+        px = _addr("x", x, (dt,), (R, K), dev)
+        pw = _addr("w", w, (dt,), (E, N, K), dev)
+        po = _addr("offsets", offsets, (torch.int32,), (E + 1,), dev)
+        c = MoeMmCfg(R, N, K, E, 0, _DT[dt], _DT[dt], 1)
+        dx = dw = None
+        if ctx.needs_input_grad[0]:
+            dx = x.new_empty(x.shape)
+            _call("moe_grouped_mm_dgrad", dev.index, C.byref(c), pd, pw, po, dx.data_ptr() or None)
+        if ctx.needs_input_grad[1]:
+            dw = w.new_empty(w.shape)
+            need = _wgrad_bytes(c)
+            work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+            _call("moe_grouped_mm_wgrad", dev.index, C.byref(c), pd, px, po, dw.data_ptr(),
+                  None if work is None else work.data_ptr(), need)
         return dx, dw, None
 
 
@@ -636,7 +651,7 @@ def moe_mm_i8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Te
     R, pt = _row_token(row_token, T, dev)
     if out is not None and out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
-    out, clear = _new_or_checked(out, (R, N), out_dtype or torch.bfloat16, tuple(_DT), dev)
+    out, clear = _new_or_checked(out, (R, N), out_dtype or torch.bfloat16, tuple(_DT), xq)
     py = _addr("out", out, tuple(_DT), (R, N), dev)
     c = MoeMmCfg(R, N, K, E, T, 0, _DT[out.dtype], clear)
     _call("moe_mm_i8", dev.index, C.byref(c), pq, ps, pw, pws, po, pt, py)
@@ -669,7 +684,7 @@ def moe_linear_i8(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets: 
     R, pt = _row_token(row_token, T, dev)
     if out is not None and out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
-    out, clear = _new_or_checked(out, (R, N), out_dtype or x.dtype, tuple(_DT), dev)
+    out, clear = _new_or_checked(out, (R, N), out_dtype or x.dtype, tuple(_DT), x)
     py = _addr("out", out, tuple(_DT), (R, N), dev)
     c = MoeMmCfg(R, N, K, E, T, _DT[x.dtype], _DT[out.dtype], clear)
     if work is None:

@@ -305,6 +305,10 @@ def test_autograd_equals_the_gradient_products(dtype):
     assert torch.equal(w2.grad, once + once)
     with torch.no_grad():
         assert not moe.moe_grouped_mm(x, w, o).requires_grad
+    # once differentiable: a gradient of the gradient is refused, not wrong
+    g1, = torch.autograd.grad(moe.moe_grouped_mm(x, w, o).float().square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(g1.float().sum(), w)
 
 
 def test_gradients_against_differences():
