@@ -93,6 +93,12 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// 16 bytes per lane to base + off, past the caches; nothing for kOutside.
+__device__ __forceinline__ void store16(uint8_t* base, const v4i& v, uint32_t off) {
+  auto r = __builtin_amdgcn_make_buffer_rsrc(base, 0, 0x7FFFFFFF, 0x00020000);
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 2);
+}
+
 // A group's rows and the tile's place in it.
 struct Place {
   int e;      // group; E and E + 1: the rows behind the last and before the first one (clear_rest)
@@ -299,8 +305,14 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
   // Each is needed a step later than its loads go out, so a third one gives
   // loads that miss the L2 two steps' time.  (Ragged groups, 32768 rows, 4096
   // -> 1536, E=64: two stages of both 482 us, a third of q 435; 2048 -> 1408:
-  // dx 157 against 133; nothing where all is in the L2.)
-  constexpr int NP = BM == 128 ? 3 : 2, NQ = BM == 64 ? 2 : 3;
+  // dx 157 against 133; nothing where all is in the L2, and nothing for dW.)
+  constexpr int NP = BM == 128 ? 3 : 2, NQ = BM == 64 || OP == kWgrad ? 2 : 3;
+  // dW's reductions are short (a group's rows), so its workgroups take several
+  // tiles in turn: the next one's first stages load while one is stored from
+  // pieces of LDS of its own.  (us, against a workgroup per tile: 64 groups of
+  // 190 rows 129 and 141, of 150 220 and 246, of 8 149 and 170, 16 of 1024 254 and
+  // 264; 64 of 512 499 and 487, where the fixed turns balance less well.)
+  constexpr bool kTurns = OP == kWgrad;
   // one array per stage: the compiler's alias analysis then keeps a stage's
   // reads free of waits for the other stage's loads
   __shared__ __align__(1024) uint8_t p0[PS::kBytes];
@@ -309,6 +321,7 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
   __shared__ __align__(1024) uint8_t q0[QS::kBytes];
   __shared__ __align__(1024) uint8_t q1[QS::kBytes];
   __shared__ __align__(1024) uint8_t q2[NQ > 2 ? QS::kBytes : 16];
+  __shared__ __align__(1024) uint8_t pieces[kTurns ? kThreads / 64 * 2048 : 16];
 
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = w >> 2, wn = w & 3;
@@ -316,33 +329,42 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
   const int ncol = (cols + kBN - 1) / kBN;
 
   Place pl;
-  int ct, red, split = 0;  // column tile, reduction length, share of the group's rows
+  int ct, red = 0, split = 0;  // column tile, reduction length, share of the group's rows
   PS ps;
   QS qs;
   const uint8_t* P = static_cast<const uint8_t*>(a.p);
   const uint8_t* Q = static_cast<const uint8_t*>(a.q);
-  if constexpr (OP == kWgrad) {
-    // tile of group e: rows are N, columns K.  Groups differ in length, so every
-    // XCD takes a run of each group's tiles (all rows of a column first, which
-    // share the column's strip of x); the first XCD moves on with the group.  A
-    // group's rows may be split over a.splits workgroups, in whole steps.
+  // kWgrad: tile of group e: rows are N, columns K.  Groups differ in length, so
+  // every XCD takes a run of each group's tiles (all rows of a column first,
+  // which share the column's strip of x); the first XCD moves on with the group.
+  // A group's rows may be split over a.splits workgroups, in whole steps.
+  // turn: the tile's number on this XCD; false behind the last one.
+  auto place_wgrad = [&](uint32_t& turn) __attribute__((always_inline)) {
     const uint32_t nrow = (a.N + BM - 1) / BM, one = nrow * ncol, run = (one + 7) / 8;
-    const uint32_t part = (blockIdx.x >> 3) / run;
-    const uint32_t in = ((blockIdx.x + part) & 7) * run + (blockIdx.x >> 3) - part * run;
-    if (part >= uint32_t(a.E) * a.splits || in >= one) return;
-    pl.e = int(part / a.splits);
-    split = int(part - pl.e * uint32_t(a.splits));
-    ct = int(in / nrow);
-    pl.row0 = int(in % nrow) * BM;
-    pl.rows = min(BM, a.N - pl.row0);
-    const int2 r = group_rows(a.offsets, pl.e, a.E, a.R);
-    const int all = r.y - r.x, each = ((all + kStep - 1) / kStep + a.splits - 1) / a.splits * kStep;
-    const int skip = int(min(long(split) * each, long(all)));
-    const int ra = __builtin_amdgcn_readfirstlane(r.x + skip);
-    red = __builtin_amdgcn_readfirstlane(min(each, all - skip));
-    ps.init(P + (long(ra) * a.N + pl.row0) * 2, (long(red) * a.N - pl.row0) * 2, long(a.N) * 2, w, lane, nullptr, 0, 0);
-    qs.init(Q + (long(ra) * a.K + ct * kBN) * 2, (long(red) * a.K - ct * kBN) * 2, long(a.K) * 2, w, lane, nullptr, 0,
-            0);
+    for (;; turn += gridDim.x >> 3) {
+      const uint32_t part = turn / run;
+      if (part >= uint32_t(a.E) * a.splits) return false;
+      const uint32_t in = ((blockIdx.x + part) & 7) * run + turn - part * run;
+      if (in >= one) continue;  // the runs of the last XCDs are shorter
+      pl.e = int(part / a.splits);
+      split = int(part - pl.e * uint32_t(a.splits));
+      ct = int(in / nrow);
+      pl.row0 = int(in % nrow) * BM;
+      pl.rows = min(BM, a.N - pl.row0);
+      const int2 r = group_rows(a.offsets, pl.e, a.E, a.R);
+      const int all = r.y - r.x, each = ((all + kStep - 1) / kStep + a.splits - 1) / a.splits * kStep;
+      const int skip = int(min(long(split) * each, long(all)));
+      const int ra = __builtin_amdgcn_readfirstlane(r.x + skip);
+      red = __builtin_amdgcn_readfirstlane(min(each, all - skip));
+      ps.init(P + (long(ra) * a.N + pl.row0) * 2, (long(red) * a.N - pl.row0) * 2, long(a.N) * 2, w, lane, nullptr, 0, 0);
+      qs.init(Q + (long(ra) * a.K + ct * kBN) * 2, (long(red) * a.K - ct * kBN) * 2, long(a.K) * 2, w, lane, nullptr, 0,
+              0);
+      return true;
+    }
+  };
+  uint32_t turn = blockIdx.x >> 3;
+  if constexpr (OP == kWgrad) {
+    if (!place_wgrad(turn)) return;
   } else {
     if (!find_tile(a, BM, ncol, blockIdx.x, pl, ct)) return;
     red = OP == kFwd ? a.K : a.N;
@@ -361,14 +383,7 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
       qs.left = 0;
     }
   }
-  const int steps = (red + kStep - 1) / kStep;
-
   typename Acc<TY>::type acc[MF][NF];
-#pragma unroll
-  for (int i = 0; i < MF; ++i)
-#pragma unroll
-    for (int j = 0; j < NF; ++j) acc[i][j] = typename Acc<TY>::type{0, 0, 0, 0};
-
   int kleft_p = OP == kWgrad ? 0 : red * kEl, kleft_q = kleft_p;  // bytes of a C row from the next step to load on
   auto issue_p = [&](uint8_t* sp) __attribute__((always_inline)) {
     ps.issue(sp, w, kleft_p);
@@ -418,116 +433,147 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
       __builtin_amdgcn_sched_group_barrier(0x008, MF * NF / 8, 0);
     }
   };
-  // in the order of the steps: p(s), q(s + NQ - 2), p(s + 1), ... (see step)
-  issue_p(p0);
-  issue_q(q0);
-  if constexpr (NQ > NP) issue_q(q1);
-  issue_p(p1);
-  issue_q(NQ > NP ? q2 : q1);
-  if constexpr (NP > 2) {
-    issue_p(p2);
-    issue_q(q2);
-  }
-  stage_barrier_but<(NP - 1) * PS::kLoads + (NQ - 1) * QS::kLoads>();
-  read(even, p0, q0, 0);
-  int s = 0;
-  if constexpr (NQ == 2) {
-    for (; s + 1 < steps; s += 2) {
-      step(p0, q0, p1, q1);
-      step(p1, q1, p0, q0);
+  auto start = [&]() __attribute__((always_inline)) {
+    // in the order of the steps: p(s), q(s + NQ - 2), p(s + 1), ... (see step)
+    issue_p(p0);
+    issue_q(q0);
+    if constexpr (NQ > NP) issue_q(q1);
+    issue_p(p1);
+    issue_q(NQ > NP ? q2 : q1);
+    if constexpr (NP > 2) {
+      issue_p(p2);
+      issue_q(q2);
     }
-    if (s < steps) step(p0, q0, p1, q1);
-  } else if constexpr (NP == 3) {
-    for (; s + 2 < steps; s += 3) {
-      step(p0, q0, p1, q1);
-      step(p1, q1, p2, q2);
-      step(p2, q2, p0, q0);
-    }
-    if (s < steps) {
-      step(p0, q0, p1, q1);
-      if (s + 1 < steps) step(p1, q1, p2, q2);
-    }
-  } else {
-    for (; s + 5 < steps; s += 6) {
-      step(p0, q0, p1, q1);
-      step(p1, q1, p0, q2);
-      step(p0, q2, p1, q0);
-      step(p1, q0, p0, q1);
-      step(p0, q1, p1, q2);
-      step(p1, q2, p0, q0);
-    }
-    if (s < steps) {
-      step(p0, q0, p1, q1);
-      if (s + 1 < steps) {
+  };
+  // 16-bit stores of a wave and tile: two per 16 rows (fp32: twice as many)
+  constexpr int kStores = 2 * MF;
+  constexpr int kAhead = (NP - 1) * PS::kLoads + (NQ - 1) * QS::kLoads;
+  static_assert(kAhead + kStores < 64, "vmcnt range");
+  start();
+  bool stored = false;  // the tile before is still being stored, in kStores stores
+  for (;;) {
+    // the first stage has arrived: all but the other stages' loads, and the
+    // stores behind them, are complete
+    if (kTurns && stored) stage_barrier_but<kAhead + kStores>();
+    else stage_barrier_but<kAhead>();
+    const int steps = (red + kStep - 1) / kStep;
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; ++j) acc[i][j] = typename Acc<TY>::type{0, 0, 0, 0};
+    read(even, p0, q0, 0);
+    int s = 0;
+    if constexpr (NQ == 2) {
+      for (; s + 1 < steps; s += 2) {
+        step(p0, q0, p1, q1);
+        step(p1, q1, p0, q0);
+      }
+      if (s < steps) step(p0, q0, p1, q1);
+    } else if constexpr (NP == 3) {
+      for (; s + 2 < steps; s += 3) {
+        step(p0, q0, p1, q1);
+        step(p1, q1, p2, q2);
+        step(p2, q2, p0, q0);
+      }
+      if (s < steps) {
+        step(p0, q0, p1, q1);
+        if (s + 1 < steps) step(p1, q1, p2, q2);
+      }
+    } else {
+      for (; s + 5 < steps; s += 6) {
+        step(p0, q0, p1, q1);
         step(p1, q1, p0, q2);
-        if (s + 2 < steps) {
-          step(p0, q2, p1, q0);
-          if (s + 3 < steps) {
-            step(p1, q0, p0, q1);
-            if (s + 4 < steps) step(p0, q1, p1, q2);
+        step(p0, q2, p1, q0);
+        step(p1, q0, p0, q1);
+        step(p0, q1, p1, q2);
+        step(p1, q2, p0, q0);
+      }
+      if (s < steps) {
+        step(p0, q0, p1, q1);
+        if (s + 1 < steps) {
+          step(p1, q1, p0, q2);
+          if (s + 2 < steps) {
+            step(p0, q2, p1, q0);
+            if (s + 3 < steps) {
+              step(p1, q0, p0, q1);
+              if (s + 4 < steps) step(p0, q1, p1, q2);
+            }
           }
         }
       }
     }
-  }
 
-  // Lane l holds columns 4 (l / 16) + 0..3 of row l % 16 of each fragment.
-  // Sixteen rows at a time go through a piece of LDS of the wave's own, so that
-  // a store covers whole rows of its 64 columns (128 or 256 bytes in a line)
-  // instead of 32-byte pieces, and past the caches (268 MB of bf16 gradients, 16
-  // groups of 1024 rows: 90 us less than in pieces).
-  stage_barrier();  // no stage is read or filled any more
-  int el = lane;
-  asm volatile("" : "+v"(el));  // addresses from here on are not formed before the loop, which has no registers for them
-  const int m = el & 15, g = el >> 4;
-  const long out_row0 = OP == kWgrad ? long(pl.e) * a.N + pl.row0 : long(pl.row0);
-  const int out_ty = OP == kWgrad && a.splits > 1 ? kFp32 : a.out_ty;
-  void* out = OP == kWgrad && a.splits > 1 ? a.partial + long(split) * a.E * a.N * a.K : a.out;
-  const int r0 = wm * (BM / 2), c0 = ct * kBN + wn * 16 * NF;
-  static_assert(QS::kBytes >= kThreads / 64 * 4096, "a piece of 4 KB per wave");
-#pragma unroll
-  for (int i = 0; i < MF; ++i) {
-    uint8_t* piece = (i & 1 ? q1 : q0) + w * 4096;
-    v4f v[NF];
-#pragma unroll
-    for (int j = 0; j < NF; ++j) {
-      const int r = r0 + i * 16 + m, c = c0 + j * 16 + 4 * g;
-      v[j] = TY == kInt8 && (r >= pl.rows || c >= cols) ? v4f{0.0f, 0.0f, 0.0f, 0.0f}
-                                                        : scaled<TY>(a, pl.e, pl.row0 + r, c, acc[i][j]);
+    // Lane l holds columns 4 (l / 16) + 0..3 of row l % 16 of each fragment.
+    // Sixteen rows at a time go through a piece of LDS of the wave's own, so that
+    // a store covers whole rows of its 64 columns (128 or 256 bytes in a line)
+    // instead of 32-byte pieces, and past the caches (268 MB of bf16 gradients, 16
+    // groups of 1024 rows: 90 us less than in pieces).
+    stage_barrier();  // no stage is read or filled any more
+    const Place done = pl;
+    const int done_ct = ct, done_split = split;
+    bool more = false;
+    if constexpr (kTurns) {
+      turn += gridDim.x >> 3;
+      more = place_wgrad(turn);
+      if (more) start();
     }
-    // rows of 128 (256) bytes, their 16-byte chunks exchanged by the row's
-    // number so that the 16 rows' equal columns lie on different banks
-    if (out_ty == kFp32) {
+    int el = lane;
+    asm volatile("" : "+v"(el));  // addresses from here on are not formed before the loop, which has no registers for them
+    const int m = el & 15, g = el >> 4;
+    const long out_row0 = OP == kWgrad ? long(done.e) * a.N + done.row0 : long(done.row0);
+    const int out_ty = OP == kWgrad && a.splits > 1 ? kFp32 : a.out_ty;
+    void* out = OP == kWgrad && a.splits > 1 ? a.partial + long(done_split) * a.E * a.N * a.K : a.out;
+    const int r0 = wm * (BM / 2), c0 = done_ct * kBN + wn * 16 * NF;
+    uint8_t* rows0 = static_cast<uint8_t*>(out) + (out_row0 + r0) * cols * (out_ty == kFp32 ? 4 : 2);
 #pragma unroll
-      for (int j = 0; j < NF; ++j) *reinterpret_cast<v4f*>(piece + m * 256 + (((4 * j + g) ^ m) << 4)) = v[j];
-    } else {
+    for (int i = 0; i < MF; ++i) {
+      v4f v[NF];
 #pragma unroll
-      for (int j = 0; j < NF; ++j)
-        *reinterpret_cast<uint2*>(piece + m * 128 + (((2 * j + (g >> 1)) ^ (m & 7)) << 4) + (g & 1) * 8) =
-            round4(v[j], out_ty);
-    }
-    __builtin_amdgcn_wave_barrier();
-    if (out_ty == kFp32) {
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const int row = h * 4 + (el >> 4), ch = el & 15;
-        const v4i d = *reinterpret_cast<const v4i*>(piece + row * 256 + ((ch ^ row) << 4));
-        const int r = r0 + i * 16 + row, c = c0 + ch * 4;
-        if (r < pl.rows && c < cols)
-          __builtin_nontemporal_store(d, reinterpret_cast<v4i*>(static_cast<float*>(out) + (out_row0 + r) * cols + c));
+      for (int j = 0; j < NF; ++j) {
+        const int r = r0 + i * 16 + m, c = c0 + j * 16 + 4 * g;
+        v[j] = TY == kInt8 && (r >= done.rows || c >= cols) ? v4f{0.0f, 0.0f, 0.0f, 0.0f}
+                                                            : scaled<TY>(a, done.e, done.row0 + r, c, acc[i][j]);
       }
-    } else {
+      uint8_t* piece = kTurns ? pieces + w * 2048 : (i & 1 ? q1 : q0) + w * 2048;
+      // rows of 128 (256) bytes, their 16-byte chunks exchanged by the row's
+      // number so that equal columns of different rows lie on different banks
+      if (out_ty == kFp32) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = h * 8 + (el >> 3), ch = el & 7;
-        const v4i d = *reinterpret_cast<const v4i*>(piece + row * 128 + ((ch ^ (row & 7)) << 4));
-        const int r = r0 + i * 16 + row, c = c0 + ch * 8;
-        if (r < pl.rows && c < cols)
-          __builtin_nontemporal_store(d,
-                                      reinterpret_cast<v4i*>(static_cast<uint16_t*>(out) + (out_row0 + r) * cols + c));
+        for (int u = 0; u < 2; ++u) {  // eight rows at a time
+          if ((m >> 3) == u) {
+#pragma unroll
+            for (int j = 0; j < NF; ++j)
+              *reinterpret_cast<v4f*>(piece + (m & 7) * 256 + (((4 * j + g) ^ (m & 7)) << 4)) = v[j];
+          }
+          __builtin_amdgcn_wave_barrier();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int row = h * 4 + (el >> 4), ch = el & 15;
+            const v4i d = *reinterpret_cast<const v4i*>(piece + row * 256 + ((ch ^ row) << 4));
+            const int r = i * 16 + u * 8 + row, c = c0 + ch * 4;
+            store16(rows0, d, r0 + r < done.rows && c < cols ? uint32_t(r * cols + c) * 4 : kOutside);
+          }
+          __builtin_amdgcn_wave_barrier();
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+          *reinterpret_cast<uint2*>(piece + m * 128 + (((2 * j + (g >> 1)) ^ (m & 7)) << 4) + (g & 1) * 8) =
+              round4(v[j], out_ty);
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = h * 8 + (el >> 3), ch = el & 7;
+          const v4i d = *reinterpret_cast<const v4i*>(piece + row * 128 + ((ch ^ (row & 7)) << 4));
+          const int r = i * 16 + row, c = c0 + ch * 8;
+          store16(rows0, d, r0 + r < done.rows && c < cols ? uint32_t(r * cols + c) * 2 : kOutside);
+        }
+        __builtin_amdgcn_wave_barrier();
       }
     }
-    __builtin_amdgcn_wave_barrier();
+    if (!more) break;
+    stored = out_ty != kFp32;
+    if (!stored) wait_vm<0>();
   }
 }
 
@@ -891,7 +937,10 @@ size_t wgrad_bytes(const MmArgs& a) {
 // Workgroups of a launch in the given shape (64-bit: the ABI refuses more than 2^31).
 static long grid_of(int op, const MmArgs& a, const TileShape& s) {
   const long cols = op == kFwd ? a.N : a.K, ncol = (cols + s.cols - 1) / s.cols;
-  if (op == kWgrad) return ((a.N + s.rows - 1) / s.rows * ncol + 7) / 8 * 8 * a.E * a.splits;
+  if (op == kWgrad) {
+    const long tiles = ((a.N + s.rows - 1) / s.rows * ncol + 7) / 8 * 8 * a.E * a.splits;
+    return tiles < long(kCUs) ? tiles : long(kCUs);  // taken in turns
+  }
   return (row_tiles(a, s.rows) * ncol + 7) / 8 * 8;
 }
 
