@@ -307,11 +307,8 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
   // -> 1536, E=64: two stages of both 482 us, a third of q 435; 2048 -> 1408:
   // dx 157 against 133; nothing where all is in the L2, and nothing for dW.)
   constexpr int NP = BM == 128 ? 3 : 2, NQ = BM == 64 || OP == kWgrad ? 2 : 3;
-  // dW's reductions are short (a group's rows), so its workgroups take several
-  // tiles in turn: the next one's first stages load while one is stored from
-  // pieces of LDS of its own.  (us, against a workgroup per tile: 64 groups of
-  // 190 rows 129 and 141, of 150 220 and 246, of 8 149 and 170, 16 of 1024 254 and
-  // 264; 64 of 512 499 and 487, where the fixed turns balance less well.)
+  // dW's workgroups may take several tiles in turn: the next one's first stages
+  // load while one is stored from pieces of LDS of its own (see workgroups_of).
   constexpr bool kTurns = OP == kWgrad;
   // one array per stage: the compiler's alias analysis then keeps a stage's
   // reads free of waits for the other stage's loads
@@ -334,33 +331,33 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
   QS qs;
   const uint8_t* P = static_cast<const uint8_t*>(a.p);
   const uint8_t* Q = static_cast<const uint8_t*>(a.q);
-  // kWgrad: tile of group e: rows are N, columns K.  Groups differ in length, so
-  // every XCD takes a run of each group's tiles (all rows of a column first,
-  // which share the column's strip of x); the first XCD moves on with the group.
-  // A group's rows may be split over a.splits workgroups, in whole steps.
+  // kWgrad: tile of group e: rows are N, columns K.  All tiles have one number
+  // (group, share of its rows, column, row: those of a column share its strip of
+  // x), and runs of them are dealt to the XCDs.  Groups differ in length, so a run
+  // is an eighth of a group's tiles; where every workgroup has one tile, it is an
+  // eighth of all.  A group's rows may be split over a.splits workgroups, in whole steps.
   // turn: the tile's number on this XCD; false behind the last one.
-  auto place_wgrad = [&](uint32_t& turn) __attribute__((always_inline)) {
-    const uint32_t nrow = (a.N + BM - 1) / BM, one = nrow * ncol, run = (one + 7) / 8;
-    for (;; turn += gridDim.x >> 3) {
-      const uint32_t part = turn / run;
-      if (part >= uint32_t(a.E) * a.splits) return false;
-      const uint32_t in = ((blockIdx.x + part) & 7) * run + turn - part * run;
-      if (in >= one) continue;  // the runs of the last XCDs are shorter
-      pl.e = int(part / a.splits);
-      split = int(part - pl.e * uint32_t(a.splits));
-      ct = int(in / nrow);
-      pl.row0 = int(in % nrow) * BM;
-      pl.rows = min(BM, a.N - pl.row0);
-      const int2 r = group_rows(a.offsets, pl.e, a.E, a.R);
-      const int all = r.y - r.x, each = ((all + kStep - 1) / kStep + a.splits - 1) / a.splits * kStep;
-      const int skip = int(min(long(split) * each, long(all)));
-      const int ra = __builtin_amdgcn_readfirstlane(r.x + skip);
-      red = __builtin_amdgcn_readfirstlane(min(each, all - skip));
-      ps.init(P + (long(ra) * a.N + pl.row0) * 2, (long(red) * a.N - pl.row0) * 2, long(a.N) * 2, w, lane, nullptr, 0, 0);
-      qs.init(Q + (long(ra) * a.K + ct * kBN) * 2, (long(red) * a.K - ct * kBN) * 2, long(a.K) * 2, w, lane, nullptr, 0,
-              0);
-      return true;
-    }
+  auto place_wgrad = [&](uint32_t turn) __attribute__((always_inline)) {
+    const uint32_t nrow = (a.N + BM - 1) / BM, one = nrow * ncol, total = one * a.E * a.splits;
+    const uint32_t run = ((total <= uint32_t(kCUs) ? total : one) + 7) / 8;
+    const uint32_t f = (turn / run * 8 + (blockIdx.x & 7)) * run + turn % run;
+    // (the last runs of an XCD may lie behind the end: so do all its turns from there on)
+    if (f >= total) return false;
+    const uint32_t part = f / one, in = f - part * one;
+    pl.e = int(part / a.splits);
+    split = int(part - pl.e * uint32_t(a.splits));
+    ct = int(in / nrow);
+    pl.row0 = int(in % nrow) * BM;
+    pl.rows = min(BM, a.N - pl.row0);
+    const int2 r = group_rows(a.offsets, pl.e, a.E, a.R);
+    const int all = r.y - r.x, each = ((all + kStep - 1) / kStep + a.splits - 1) / a.splits * kStep;
+    const int skip = int(min(long(split) * each, long(all)));
+    const int ra = __builtin_amdgcn_readfirstlane(r.x + skip);
+    red = __builtin_amdgcn_readfirstlane(min(each, all - skip));
+    ps.init(P + (long(ra) * a.N + pl.row0) * 2, (long(red) * a.N - pl.row0) * 2, long(a.N) * 2, w, lane, nullptr, 0, 0);
+    qs.init(Q + (long(ra) * a.K + ct * kBN) * 2, (long(red) * a.K - ct * kBN) * 2, long(a.K) * 2, w, lane, nullptr, 0,
+            0);
+    return true;
   };
   uint32_t turn = blockIdx.x >> 3;
   if constexpr (OP == kWgrad) {
@@ -938,8 +935,8 @@ size_t wgrad_bytes(const MmArgs& a) {
 static long grid_of(int op, const MmArgs& a, const TileShape& s) {
   const long cols = op == kFwd ? a.N : a.K, ncol = (cols + s.cols - 1) / s.cols;
   if (op == kWgrad) {
-    const long tiles = ((a.N + s.rows - 1) / s.rows * ncol + 7) / 8 * 8 * a.E * a.splits;
-    return tiles < long(kCUs) ? tiles : long(kCUs);  // taken in turns
+    const long tiles = (a.N + s.rows - 1) / s.rows * ncol * a.E * a.splits;
+    return (tiles + 7) / 8 * 8;
   }
   return (row_tiles(a, s.rows) * ncol + 7) / 8 * 8;
 }
@@ -977,9 +974,22 @@ static hipError_t launch_shape(const MmArgs& a, const TileShape& s, unsigned gri
 }
 #undef MOE_MM
 
+// Workgroups of kWgrad: one per tile, or one per CU that takes its tiles in turn.
+// Turns hide a tile's first loads and its stores, which counts where reductions
+// are short; but they are dealt out beforehand, so the last round's empty places
+// cost their whole length, and long groups are not evened out.  (us, turns and one
+// per tile: 64 groups, 1408 x 2048, 12 tiles per CU, of 16 rows 89 and 108, 192 132 and
+// 143, 512 237 and 245, 768 357 and 345; 1536 x 4096 of 256 283 and 308, 512 486 and
+// 480; 768 x 768, 2.25 per CU, of 128 32 and 34, 192 39 and 38, 256 46 and 41, 1024 119 and 93.)
+static unsigned workgroups_of(const MmArgs& a, long tiles) {
+  const double rows = double(a.R) / (double(a.E) * a.splits), each = tiles / kCUs;
+  const bool turns = each > 1 && rows <= 256 && rows * (std::ceil(each) / each - 1) < 64;
+  return unsigned(turns ? long(kCUs) : tiles);
+}
+
 static hipError_t launch_one(int op, const MmArgs& a, const TileShape& s, long grid, hipStream_t st) {
   if (grid == 0) return hipSuccess;
-  const unsigned g = unsigned(grid);
+  const unsigned g = op == kWgrad ? workgroups_of(a, grid) : unsigned(grid);
   if (a.ty == kInt8) return launch_shape<kFwd, kInt8>(a, s, g, st);
   if (a.ty == kBf16)
     return op == kFwd ? launch_shape<kFwd, kBf16>(a, s, g, st)

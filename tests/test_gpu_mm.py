@@ -276,6 +276,29 @@ def test_int8_rows_past_32_bits():
 
 
 # ------------------------------------------------------------------ autograd
+@pytest.mark.parametrize("out", [BF16, FP16, FP32], ids=["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("E,N,K,rows", [(40, 776, 520, 20), (300, 264, 264, 9), (530, 8, 8, 3), (70, 1032, 264, 130),
+                                        (30, 2056, 264, 300), (3, 520, 776, 1500), (1, 520, 520, 4000)],
+                         ids=lambda v: str(v))
+def test_wgrad_many_tiles(E, N, K, rows, out):
+    """More tiles than CUs, with short reductions (one workgroup takes several
+    tiles) and long ones, tile counts that no power of two divides, empty and
+    long groups in between; and fewer tiles, whose rows are split."""
+    g = gen(77)
+    counts = [0 if E > 1 and e % 5 == 2 else rows * (3 if e % 7 == 3 else 1) - e % 3 for e in range(E)]
+    o, R = offs(counts), sum(counts)
+    dtype = FP16 if out == FP16 else BF16
+    dy, x = rand(g, R, N, dtype=dtype), rand(g, R, K, dtype=dtype)
+    ref, mag = ref_wgrad(dy, x, o)
+    dw = torch.full((E, N, K), float("nan"), dtype=out, device=DEV)
+    note(E, N, K, R, out)
+    for _ in range(3):
+        dw.fill_(float("nan"))
+        M().moe_grouped_mm_wgrad(dy, x, o, out=dw)
+        near(dw, ref, mag, max(counts), "dW")
+    assert torch.equal(dw, M().moe_grouped_mm_wgrad(dy, x, o, out=torch.empty_like(dw)))
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
 def test_autograd_equals_the_gradient_products(dtype):
     moe = M()
