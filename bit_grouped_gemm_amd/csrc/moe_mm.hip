@@ -292,7 +292,12 @@ __device__ __forceinline__ v4i read_frag(const uint8_t* stage, int frag, int kk,
   }
 }
 
-template <int OP, int TY, int BM>
+// Tiles of the weight gradient that an XCD takes in a run, of `one` in a group
+// and `total` of all.  Groups differ in length, so it is an eighth of a group's;
+// where every workgroup has one tile, it is an eighth of all.
+__host__ __device__ constexpr long run_of(long one, long total) { return ((total <= long(kCUs) ? total : one) + 7) / 8; }
+
+template <int OP, int TY, int BM, bool kTurns = false>
 __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
   constexpr bool PT = OP == kWgrad, QT = OP != kFwd;
   constexpr int NF = 4;             // column fragments of a wave (64 columns)
@@ -305,11 +310,12 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
   // Each is needed a step later than its loads go out, so a third one gives
   // loads that miss the L2 two steps' time.  (Ragged groups, 32768 rows, 4096
   // -> 1536, E=64: two stages of both 482 us, a third of q 435; 2048 -> 1408:
-  // dx 157 against 133; nothing where all is in the L2, and nothing for dW.)
-  constexpr int NP = BM == 128 ? 3 : 2, NQ = BM == 64 || OP == kWgrad ? 2 : 3;
-  // dW's workgroups may take several tiles in turn: the next one's first stages
-  // load while one is stored from pieces of LDS of its own (see workgroups_of).
-  constexpr bool kTurns = OP == kWgrad;
+  // dx 157 against 133; dW of 16 groups of 1024, 2048 -> 4096, cold operands, 302 against 285;
+  // nothing where all is in the L2.)
+  // kTurns: a workgroup takes several tiles of dW in turn, and the next one's first
+  // stages load while one is stored from pieces of LDS of its own, which take
+  // the third stage's place (see takes_turns).
+  constexpr int NP = BM == 128 ? 3 : 2, NQ = BM == 64 || kTurns ? 2 : 3;
   // one array per stage: the compiler's alias analysis then keeps a stage's
   // reads free of waits for the other stage's loads
   __shared__ __align__(1024) uint8_t p0[PS::kBytes];
@@ -333,13 +339,12 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
   const uint8_t* Q = static_cast<const uint8_t*>(a.q);
   // kWgrad: tile of group e: rows are N, columns K.  All tiles have one number
   // (group, share of its rows, column, row: those of a column share its strip of
-  // x), and runs of them are dealt to the XCDs.  Groups differ in length, so a run
-  // is an eighth of a group's tiles; where every workgroup has one tile, it is an
-  // eighth of all.  A group's rows may be split over a.splits workgroups, in whole steps.
+  // x), and runs of them are dealt to the XCDs.  A group's rows may be split over
+  // a.splits workgroups, in whole steps.
   // turn: the tile's number on this XCD; false behind the last one.
   auto place_wgrad = [&](uint32_t turn) __attribute__((always_inline)) {
     const uint32_t nrow = (a.N + BM - 1) / BM, one = nrow * ncol, total = one * a.E * a.splits;
-    const uint32_t run = ((total <= uint32_t(kCUs) ? total : one) + 7) / 8;
+    const uint32_t run = run_of(one, total);
     const uint32_t f = (turn / run * 8 + (blockIdx.x & 7)) * run + turn % run;
     // (the last runs of an XCD may lie behind the end: so do all its turns from there on)
     if (f >= total) return false;
@@ -935,10 +940,24 @@ size_t wgrad_bytes(const MmArgs& a) {
 static long grid_of(int op, const MmArgs& a, const TileShape& s) {
   const long cols = op == kFwd ? a.N : a.K, ncol = (cols + s.cols - 1) / s.cols;
   if (op == kWgrad) {
-    const long tiles = (a.N + s.rows - 1) / s.rows * ncol * a.E * a.splits;
-    return (tiles + 7) / 8 * 8;
+    const long one = (a.N + s.rows - 1) / s.rows * ncol, total = one * a.E * a.splits;
+    const long runs = 8 * run_of(one, total);  // one of each XCD
+    return (total + runs - 1) / runs * runs;
   }
   return (row_tiles(a, s.rows) * ncol + 7) / 8 * 8;
+}
+
+// kWgrad: whether a workgroup per CU takes the tiles in turn, rather than one
+// workgroup per tile.  Turns hide a tile's first loads and its stores, which
+// counts where reductions are short; but they cost the third stage, the last
+// round's empty places cost their whole length, and long groups are not evened out.
+// (Cold operands, us, turns and one per tile: 64 groups, 1408 x 2048, 12 tiles per CU,
+// of 16 rows 87 and 98, 128 116 and 123, 256 186 and 175, 1024 422 and 403; 256 groups,
+// 512 x 512, of 128 51 and 55, 192 75 and 69; 16 groups, 4096 x 2048, of 128 79 and 86, 1024
+// 311 and 267; 64 groups, 768 x 768, 2.25 per CU, of 128 33 and 34, 512 82 and 61.)
+static bool takes_turns(const MmArgs& a, long tiles) {
+  const double rows = double(a.R) / (double(a.E) * a.splits), each = tiles / kCUs;
+  return each > 1 && rows <= 128 && rows * (std::ceil(each) / each - 1) < 64;
 }
 
 #define MOE_MM(kernel, threads) hipLaunchKernelGGL((kernel), dim3(grid), dim3(threads), 0, st, a)
@@ -946,7 +965,8 @@ static long grid_of(int op, const MmArgs& a, const TileShape& s) {
 template <int OP, int TY>
 static hipError_t launch_shape(const MmArgs& a, const TileShape& s, unsigned grid, hipStream_t st) {
   if constexpr (OP == kWgrad) {
-    MOE_MM((k_mm<OP, TY, 256>), kThreads);
+    if (takes_turns(a, grid)) hipLaunchKernelGGL((k_mm<OP, TY, 256, true>), dim3(unsigned(kCUs)), dim3(kThreads), 0, st, a);
+    else MOE_MM((k_mm<OP, TY, 256>), kThreads);
     if (a.splits > 1) {
       const long n = long(a.E) * a.N * a.K, blocks = (n + 1023) / 1024;
       hipLaunchKernelGGL(k_join, dim3(unsigned(blocks < 2048 ? blocks : 2048)), dim3(256), 0, st, a.partial, a.splits, n,
@@ -974,22 +994,9 @@ static hipError_t launch_shape(const MmArgs& a, const TileShape& s, unsigned gri
 }
 #undef MOE_MM
 
-// Workgroups of kWgrad: one per tile, or one per CU that takes its tiles in turn.
-// Turns hide a tile's first loads and its stores, which counts where reductions
-// are short; but they are dealt out beforehand, so the last round's empty places
-// cost their whole length, and long groups are not evened out.  (us, turns and one
-// per tile: 64 groups, 1408 x 2048, 12 tiles per CU, of 16 rows 89 and 108, 192 132 and
-// 143, 512 237 and 245, 768 357 and 345; 1536 x 4096 of 256 283 and 308, 512 486 and
-// 480; 768 x 768, 2.25 per CU, of 128 32 and 34, 192 39 and 38, 256 46 and 41, 1024 119 and 93.)
-static unsigned workgroups_of(const MmArgs& a, long tiles) {
-  const double rows = double(a.R) / (double(a.E) * a.splits), each = tiles / kCUs;
-  const bool turns = each > 1 && rows <= 256 && rows * (std::ceil(each) / each - 1) < 64;
-  return unsigned(turns ? long(kCUs) : tiles);
-}
-
 static hipError_t launch_one(int op, const MmArgs& a, const TileShape& s, long grid, hipStream_t st) {
   if (grid == 0) return hipSuccess;
-  const unsigned g = op == kWgrad ? workgroups_of(a, grid) : unsigned(grid);
+  const unsigned g = unsigned(grid);
   if (a.ty == kInt8) return launch_shape<kFwd, kInt8>(a, s, g, st);
   if (a.ty == kBf16)
     return op == kFwd ? launch_shape<kFwd, kBf16>(a, s, g, st)
