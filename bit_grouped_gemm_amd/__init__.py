@@ -581,7 +581,9 @@ def moe_grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out:
 
     Differentiable with respect to x and w (once; not with `out` or
     `out_dtype`): the gradients are moe_grouped_mm_dgrad and
-    moe_grouped_mm_wgrad, and rows of no group get the gradient 0."""
+    moe_grouped_mm_wgrad, and rows of no group get the gradient 0.  In a graph,
+    capture forward and backward together, while no earlier result computed from
+    the same leaves is kept: PyTorch ties a leaf's gradient to the stream of its first use."""
     if (x.requires_grad or w.requires_grad) and torch.is_grad_enabled():
         if out is not None or out_dtype not in (None, x.dtype):
             raise ValueError("moe_grouped_mm: out and out_dtype cannot be given where a gradient is needed")
