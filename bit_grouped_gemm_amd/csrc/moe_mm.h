@@ -18,6 +18,12 @@ constexpr int kBf16 = 0, kFp16 = 1, kFp32 = 2, kInt8 = 3;
 //   kWgrad  dw[e][n][k] = sum_{r in e} dy[r][n] x[r][k]
 constexpr int kFwd = 0, kDgrad = 1, kWgrad = 2;
 
+// Workgroups of `threads` that one launch may have: its work items are counted
+// in 32 bits, and a count past them wraps, so that most of the grid never runs
+// and the call still succeeds.
+constexpr long max_blocks(int threads) { return ((1L << 32) - 1) / threads; }
+static_assert(max_blocks(256) * 256 < (1L << 32) && (max_blocks(256) + 1) * 256 >= (1L << 32), "limit of a launch");
+
 struct MmArgs {
   const void* p;             // x (kFwd) or dy: the operand whose index is the output's row
   const void* q;             // w, or x (kWgrad): its index is the output's column

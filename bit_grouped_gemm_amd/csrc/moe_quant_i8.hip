@@ -59,11 +59,25 @@ __global__ __launch_bounds__(256) void k_quant_i8(const uint16_t* __restrict__ x
   }
 }
 
+// One launch, or as many as the rows need: THREADS = 64 passes a launch's limit
+// at 2^26 rows (2 GB of x at K = 16), THREADS = 256 at 2^24.
+template <int TY, bool GLU, int THREADS, int NC>
+hipError_t launch_rows(const uint16_t* x, int R, int K, int8_t* codes, float* scales, hipStream_t st) {
+  constexpr int kPer = 256 / THREADS;  // rows of a workgroup
+  constexpr long kMost = max_blocks(256) * kPer;
+  for (long r0 = 0; r0 < R; r0 += kMost) {
+    const long n = R - r0 < kMost ? R - r0 : kMost;
+    hipLaunchKernelGGL((k_quant_i8<TY, GLU, THREADS, NC>), dim3(unsigned((n + kPer - 1) / kPer)), dim3(256), 0, st,
+                       x + r0 * (GLU ? 2L * K : K), int(n), K, codes + r0 * K, scales + r0);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 template <int TY, bool GLU>
 hipError_t launch_ty(const uint16_t* x, int R, int K, int8_t* codes, float* scales, hipStream_t st) {
-#define MOE_QUANT(TH, NC)                                                                                       \
-  hipLaunchKernelGGL((k_quant_i8<TY, GLU, TH, NC>), dim3((long(R) * TH + 255) / 256), dim3(256), 0, st, x, R, K, \
-                     codes, scales)
+#define MOE_QUANT(TH, NC) return launch_rows<TY, GLU, TH, NC>(x, R, K, codes, scales, st)
   // a wave per row up to 1024 values, a workgroup from there on (32768 rows:
   // K = 1024 17.4 us against 25.5, K = 2048 33.0 against 33.1, K = 4096 78
   // against 69; 488 rows of 1536, SwiGLU: 4.4 against 3.5)
@@ -75,7 +89,6 @@ hipError_t launch_ty(const uint16_t* x, int R, int K, int8_t* codes, float* scal
   else if (K <= 16384) MOE_QUANT(256, 8);
   else MOE_QUANT(256, 0);
 #undef MOE_QUANT
-  return hipGetLastError();
 }
 
 }  // namespace

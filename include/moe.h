@@ -391,7 +391,8 @@ int moe_grouped_mm_wgrad(const moe_mm_cfg* cfg, const void* dy, const void* x, c
  *   x      [R][K] of dtype; swiglu = 1: [R][2 K], v = silu(x[:, :K]) *
  *          x[:, K:] in fp32 (the layer's SwiGLU)
  *   codes  int8 [R][K]; scales fp32 [R]
- * K a multiple of 16 up to 2^20 (MOE_ERR_BAD_SHAPE otherwise). */
+ * K a multiple of 16 up to 2^20 (MOE_ERR_BAD_SHAPE otherwise); any R (more
+ * rows than a launch takes, 2^26 or for K > 1024 2^24, go out in several). */
 int moe_quant_i8(int R, int K, int dtype, int swiglu, const void* x, int8_t* codes, float* scales, void* stream);
 
 /* The int8 product: y[r][n] = (sum_k xq[t][k] * wq[e][n][k]) * xs[t] *

@@ -1,0 +1,72 @@
+"""The row-major products and the int8 quantiser at the borders of what a launch
+and an int32 hold (needs an MI355X).
+
+A launch counts its work items in 32 bits, and a larger count wraps without an
+error: so every row of these results is looked at, and what is left unwritten
+shows.  Rows that are not under test are zeros, and outputs start as something else."""
+import pytest
+import torch
+
+import bit_grouped_gemm_amd as moe
+from test_gpu_mm import BF16, DEV, FP16, FP32, codes, gen, note, rand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    moe.load()
+    yield
+
+
+@pytest.fixture(autouse=True)
+def _memory():
+    """These tests take tens of GB each."""
+    yield
+    torch.cuda.empty_cache()
+
+
+def all_equal(t, value):
+    """Every element of t, in pieces (a comparison of the whole would need as much again)."""
+    return all(bool((part == value).all()) for part in t.reshape(-1).split(1 << 30))
+
+
+# ------------------------------------------------------------------ more rows than a launch has work items
+# four rows per workgroup up to K = 1024, one beyond: 2^26 and 2^24 rows are 2^32 work items
+@pytest.mark.parametrize("R,K,swiglu", [((1 << 26) - 4, 16, False), ((1 << 26) - 3, 16, False), (1 << 26, 16, False),
+                                        ((1 << 26) + 4, 16, True), (3 * (1 << 26) + 1, 16, False),
+                                        ((1 << 24) - 1, 1040, False), (1 << 24, 1040, False), ((1 << 24) + 8, 1040, True)])
+def test_quant_i8_rows_past_a_launch(R, K, swiglu):
+    note("test_quant_i8_rows_past_a_launch", R, K, swiglu)
+    g = gen(3)
+    width = 2 * K if swiglu else K
+    x = torch.zeros(R, width, dtype=BF16, device=DEV)
+    # around the end of a first launch, and the last rows
+    border = min((1 << 26 if K <= 1024 else 1 << 24) - 4, R - 16)
+    for a in (border - 8, R - 16):
+        x[a:a + 16] = rand(g, 16, width)
+    q = torch.full((R, K), 99, dtype=torch.int8, device=DEV)
+    s = torch.full((R,), -1.0, device=DEV)
+    moe.moe_quant_i8(x, swiglu, codes=q, scales=s)
+    zero = moe.moe_quant_i8(torch.zeros(1, width, dtype=BF16, device=DEV), swiglu)[1]
+    for a in (border - 8, R - 16):
+        want = moe.moe_quant_i8(x[a:a + 16].contiguous(), swiglu)
+        assert torch.equal(q[a:a + 16], want[0]) and torch.equal(s[a:a + 16], want[1])
+    for a in (border - 8, R - 16):
+        q[a:a + 16], s[a:a + 16] = 0, zero
+    assert all_equal(q, 0) and all_equal(s, zero)
+
+
+def test_linear_i8_rows_past_a_launch():
+    g = gen(4)
+    R, K, N = (1 << 26) + 5, 16, 8
+    note("test_linear_i8_rows_past_a_launch", R)
+    x = torch.zeros(R, K, dtype=FP16, device=DEV)
+    x[-16:] = rand(g, 16, K, dtype=FP16)
+    wq, ws = codes(g, N, K), torch.rand(N, device=DEV, generator=g) * 1e-2
+    y = torch.full((R, N), 7.0, dtype=FP32, device=DEV)
+    moe.moe_linear_i8(x, wq, ws, out=y)
+    assert torch.equal(y[-16:], moe.moe_linear_i8(x[-16:].contiguous(), wq, ws, out_dtype=FP32))
+    assert all_equal(y[:-16], 0)
