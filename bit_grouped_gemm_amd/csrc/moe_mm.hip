@@ -150,7 +150,7 @@ __device__ __forceinline__ bool find_tile(const MmArgs& a, int BM, int ncol, int
     scan(e0);
     total += __builtin_amdgcn_readlane(incl, 63);
   }
-  // the ABI keeps the tiles of a launch under 2^31
+  // a launch has fewer than 2^24 tiles (see plan)
   const uint32_t tiles = uint32_t(total) * uint32_t(ncol), per = (tiles + 7) / 8;
   const uint32_t t = (id & 7) * per + (id >> 3);
   if (uint32_t(id >> 3) >= per || t >= tiles) return false;
@@ -899,6 +899,30 @@ TileShape shape_of(int op, const MmArgs& a, double* cost_of = nullptr) {
   return best;
 }
 
+// Workgroups of a launch in the given shape.
+long grid_of(int op, const MmArgs& a, const TileShape& s) {
+  const long cols = op == kFwd ? a.N : a.K, ncol = (cols + s.cols - 1) / s.cols;
+  if (op == kWgrad) {
+    const long one = (a.N + s.rows - 1) / s.rows * ncol, total = one * a.E * a.splits;
+    const long runs = 8 * run_of(one, total);  // one of each XCD
+    return (total + runs - 1) / runs * runs;
+  }
+  return (row_tiles(a, s.rows) * ncol + 7) / 8 * 8;
+}
+
+// The shape and the workgroups of a launch; false where no launch holds them.
+// shape_of takes narrow tiles for narrow products, whatever their rows (N = 8: 64
+// x 16 tiles, 2^24 workgroups at 2^30 rows); past a launch's limit it is the
+// largest ones.
+bool plan(int op, const MmArgs& a, TileShape* s, long* grid) {
+  *s = shape_of(op, a);
+  *grid = grid_of(op, a, *s);
+  if (*grid <= max_blocks(s->few ? kFewWaves * 64 : kThreads)) return true;
+  *s = {0, 256, kBN};
+  *grid = grid_of(op, a, *s);
+  return *grid <= max_blocks(kThreads);
+}
+
 // Rows of a dense product's first launch.  Where the last few rows would make
 // the large tiles go one more round, they go into a launch of their own, in the
 // shape that suits them (int8, 4099 rows, K = 7168, N = 4096, quantised: 180 us in
@@ -934,17 +958,6 @@ int splits_of(const MmArgs& a) {
 size_t wgrad_bytes(const MmArgs& a) {
   const int s = splits_of(a);
   return s > 1 ? size_t(s) * a.E * a.N * a.K * 4 : 0;
-}
-
-// Workgroups of a launch in the given shape (64-bit: the ABI refuses more than 2^31).
-static long grid_of(int op, const MmArgs& a, const TileShape& s) {
-  const long cols = op == kFwd ? a.N : a.K, ncol = (cols + s.cols - 1) / s.cols;
-  if (op == kWgrad) {
-    const long one = (a.N + s.rows - 1) / s.rows * ncol, total = one * a.E * a.splits;
-    const long runs = 8 * run_of(one, total);  // one of each XCD
-    return (total + runs - 1) / runs * runs;
-  }
-  return (row_tiles(a, s.rows) * ncol + 7) / 8 * 8;
 }
 
 // kWgrad: whether a workgroup per CU takes the tiles in turn, rather than one
@@ -1005,20 +1018,20 @@ static hipError_t launch_one(int op, const MmArgs& a, const TileShape& s, long g
                     : op == kDgrad ? launch_shape<kDgrad, kFp16>(a, s, g, st) : launch_shape<kWgrad, kFp16>(a, s, g, st);
 }
 
-constexpr long kMaxGrid = (1L << 31) - 1;
-
 bool mm_too_large(int op, const MmArgs& args) {
   MmArgs a = args;
   a.splits = op == kWgrad ? splits_of(a) : 1;
-  return grid_of(op, a, shape_of(op, a)) > kMaxGrid;
+  TileShape s;
+  long grid;
+  return !plan(op, a, &s, &grid);
 }
 
 hipError_t launch_mm(int op, const MmArgs& args, hipStream_t st, bool* too_large) {
   MmArgs a = args;
   a.splits = op == kWgrad ? splits_of(a) : 1;
-  const TileShape s = shape_of(op, a);
-  const long grid = grid_of(op, a, s);
-  *too_large = grid > kMaxGrid;
+  TileShape s;
+  long grid;
+  *too_large = !plan(op, a, &s, &grid);
   if (*too_large) return hipSuccess;
   const int rows = first_rows(op, a);
   if (rows == a.R) return launch_one(op, a, s, grid, st);
@@ -1033,9 +1046,12 @@ hipError_t launch_mm(int op, const MmArgs& args, hipStream_t st, bool* too_large
     tail.p = static_cast<const uint8_t*>(a.p) + long(rows) * a.K * el;
     if (a.ps) tail.ps = a.ps + rows;
   }
-  const TileShape hs = shape_of(op, head), ts = shape_of(op, tail);
-  const hipError_t e = launch_one(op, head, hs, grid_of(op, head, hs), st);
-  return e != hipSuccess ? e : launch_one(op, tail, ts, grid_of(op, tail, ts), st);
+  TileShape ts;
+  long tail_grid;
+  *too_large = !plan(op, head, &s, &grid) || !plan(op, tail, &ts, &tail_grid);
+  if (*too_large) return hipSuccess;
+  const hipError_t e = launch_one(op, head, s, grid, st);
+  return e != hipSuccess ? e : launch_one(op, tail, ts, tail_grid, st);
 }
 
 bool linear_is_one_launch(int R, int K) { return R <= 1 && K <= kLinMaxK; }

@@ -347,7 +347,9 @@ int moe_prepack_weights(const moe_cfg* cfg, const moe_weights* canonical, moe_we
  *   clear_rest as above.
  * Limits: N and K multiples of 8 up to 2^20 (int8: K a multiple of 16 up to
  *   2^16, which keeps every sum inside an int32), MOE_ERR_BAD_SHAPE
- *   otherwise.  R up to 2^31 - 1024; R * K and R * N may pass 2^32.
+ *   otherwise.  R up to 2^31 - 1024; R * K and R * N may pass 2^32.  A result
+ *   of more than 2^23 - 8 tiles of 256 x 256 (each group's last rows count as a
+ *   tile) is MOE_ERR_BAD_SHAPE: no launch holds them.
  * Sums are kept in fp32 (int8: exactly, in int32) and rounded once to
  * out_dtype.  Infinities and NaN stay in their row (in wgrad: in their
  * group). */

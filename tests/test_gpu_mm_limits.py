@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import bit_grouped_gemm_amd as moe
-from test_gpu_mm import BF16, DEV, FP16, FP32, codes, gen, note, rand
+from test_gpu_mm import BF16, DEV, FP16, FP32, codes, gen, near, near_i8, note, rand, ref_fwd
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +70,43 @@ def test_linear_i8_rows_past_a_launch():
     moe.moe_linear_i8(x, wq, ws, out=y)
     assert torch.equal(y[-16:], moe.moe_linear_i8(x[-16:].contiguous(), wq, ws, out_dtype=FP32))
     assert all_equal(y[:-16], 0)
+
+
+# 2^30 rows of 8 outputs are 2^24 of the 64-row tiles that narrow products take, 2^32 work items
+@pytest.mark.parametrize("R", [(1 << 30) - 192, (1 << 30) + (1 << 20) + 37])
+@pytest.mark.parametrize("name", ["moe_grouped_mm", "moe_grouped_mm_dgrad"])
+def test_products_of_more_tiles_than_a_launch(name, R):
+    note("test_products_of_more_tiles_than_a_launch", name, R)
+    g = gen(5)
+    x = torch.zeros(R, 8, dtype=BF16, device=DEV)
+    some = (0, R // 2, R - 300)  # rows that are looked at; all others are zeros
+    for a in some:
+        x[a:a + 300] = rand(g, 300, 8)
+    w = rand(g, 2, 8, 8)
+    o = torch.tensor([0, R - 200, R], dtype=torch.int32, device=DEV)
+    y = torch.full((R, 8), 7.0, dtype=BF16, device=DEV)
+    getattr(moe, name)(x, w, o, out=y)
+    wf = w if name == "moe_grouped_mm" else w.transpose(1, 2).contiguous()
+    for a in some:
+        ref, mag = ref_fwd(x[a:a + 300], wf, torch.tensor([0, 100 if a == some[2] else 300, 300]))
+        near(y[a:a + 300], ref, mag, 8, "y")
+        y[a:a + 300] = 0
+    assert all_equal(y, 0)
+
+
+@pytest.mark.parametrize("R", [(1 << 30) - 64, (1 << 30) + 64])
+def test_mm_i8_of_more_tiles_than_a_launch(R):
+    note("test_mm_i8_of_more_tiles_than_a_launch", R)
+    g = gen(6)
+    xq = torch.zeros(R, 16, dtype=torch.int8, device=DEV)
+    some = (0, R // 2, R - 300)
+    for a in some:
+        xq[a:a + 300] = codes(g, 300, 16)
+    xs = torch.full((R,), 0.5, device=DEV)
+    wq, ws = codes(g, 8, 16), torch.rand(8, device=DEV, generator=g)
+    y = torch.full((R, 8), 7.0, dtype=BF16, device=DEV)
+    moe.moe_mm_i8(xq, xs, wq, ws, out=y)
+    for a in some:
+        near_i8(y[a:a + 300], xq[a:a + 300].double() @ wq.double().t() * 0.5 * ws.double(), "y")
+        y[a:a + 300] = 0
+    assert all_equal(y, 0)
