@@ -142,15 +142,17 @@ __device__ __forceinline__ bool find_tile(const MmArgs& a, int BM, int ncol, int
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int v = __shfl_up(incl, d, 64);
-      if (lane >= d) incl += v;
+      if (lane >= d) incl = __builtin_elementwise_add_sat(incl, v);
     }
   };
   int total = 0;
   for (int e0 = 0; e0 < G; e0 += 64) {
     scan(e0);
-    total += __builtin_amdgcn_readlane(incl, 63);
+    total = __builtin_elementwise_add_sat(total, __builtin_amdgcn_readlane(incl, 63));
   }
-  // a launch has fewer than 2^24 tiles (see plan)
+  // A launch has fewer than 2^24 tiles (see plan).  Offsets that decrease can name
+  // rows many times over, and their tiles pass 32 bits: then there is none.
+  if (uint64_t(uint32_t(total)) * uint32_t(ncol) >= 0x7FFFFFFFu) return false;
   const uint32_t tiles = uint32_t(total) * uint32_t(ncol), per = (tiles + 7) / 8;
   const uint32_t t = (id & 7) * per + (id >> 3);
   if (uint32_t(id >> 3) >= per || t >= tiles) return false;

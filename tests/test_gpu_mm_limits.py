@@ -110,3 +110,22 @@ def test_mm_i8_of_more_tiles_than_a_launch(R):
         near_i8(y[a:a + 300], xq[a:a + 300].double() @ wq.double().t() * 0.5 * ws.double(), "y")
         y[a:a + 300] = 0
     assert all_equal(y, 0)
+
+
+# ------------------------------------------------------------------ wrong offsets
+@pytest.mark.parametrize("E,R", [(1024, 360_000_000), (1024, 300_000_000), (2, 1000)])
+def test_offsets_that_name_rows_many_times_stay_inside_the_tensors(E, R):
+    """Offsets 0, R, 0, R, ...: every second group claims all rows, and of 1024
+    groups their 64-row tiles pass an int32.  What comes out is not defined, but
+    nothing outside the result is written."""
+    note("test_offsets_that_name_rows_many_times", E, R)
+    g = gen(7)
+    margin = 1 << 20
+    x, w = torch.zeros(R, 8, dtype=BF16, device=DEV), rand(g, E, 8, 8)
+    o = torch.tensor([0, R] * (E // 2) + [0], dtype=torch.int32, device=DEV)
+    flat = torch.full((R + 2 * margin, 8), 5.0, dtype=BF16, device=DEV)
+    moe.moe_grouped_mm(x, w, o, out=flat[margin:margin + R])
+    torch.cuda.synchronize()
+    assert all_equal(flat[:margin], 5) and all_equal(flat[margin + R:], 5)
+    # zeros times weights, or left alone
+    assert all(bool(((p == 0) | (p == 5)).all()) for p in flat.reshape(-1).split(1 << 30))
