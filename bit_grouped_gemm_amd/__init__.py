@@ -438,6 +438,15 @@ def _addr(name: str, t: torch.Tensor, dtypes, shape, dev: torch.device):
     return _ptr(t)
 
 
+def _no_gradient(name: str, *tensors: Optional[torch.Tensor]) -> None:
+    """Refuses operands (and outputs) that need a gradient: the result would be
+    cut from their graph without a word."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{name} has no gradient: call it under torch.no_grad() or detach its operands")
+
+
 def _new_or_checked(out, shape, dtype, allowed, like):
     """The output tensor and clear_rest: a new one has every row written, a
     caller's keeps its rows of no group."""
@@ -489,7 +498,9 @@ def _grouped_mm(x, w, offsets, out=None, out_dtype=None):
 def moe_grouped_mm_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
                          out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """dx [R, K] = dy[r] @ w[e] for the rows r of each group e: moe_grouped_mm's
-    gradient with respect to x.  `out` and `out_dtype` as in moe_grouped_mm."""
+    gradient with respect to x.  `out` and `out_dtype` as in moe_grouped_mm.
+    Not differentiable: operands that need a gradient are refused."""
+    _no_gradient("moe_grouped_mm_dgrad", dy, w, out)
     _, N, K = _matrices(w)
     return _grouped("moe_grouped_mm_dgrad", "dy", dy, w, offsets, N, K, out, out_dtype)
 
@@ -501,7 +512,9 @@ def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     for an empty group): moe_grouped_mm's gradient with respect to w.
     `out_dtype`: dy's (default) or torch.float32; `out` is fully overwritten.
     `work`: uint8 scratch of at least moe_grouped_mm_wgrad_workspace_size(...)
-    bytes, allocated where absent and needed."""
+    bytes, allocated where absent and needed.  Not differentiable: operands that
+    need a gradient are refused."""
+    _no_gradient("moe_grouped_mm_wgrad", dy, x, out)
     (R, N), K, dt, dev = _rows_of("dy", dy), _rows_of("x", x)[1], dy.dtype, dy.device
     if offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError(f"offsets: shape {tuple(offsets.shape)}, expected (E + 1,)")
@@ -588,6 +601,7 @@ def moe_grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out:
         if out is not None or out_dtype not in (None, x.dtype):
             raise ValueError("moe_grouped_mm: out and out_dtype cannot be given where a gradient is needed")
         return _GroupedMM.apply(x, w, offsets)
+    _no_gradient("moe_grouped_mm with out", out)
     return _grouped_mm(x, w, offsets, out, out_dtype)
 
 
@@ -595,7 +609,9 @@ def moe_quant_i8(x: torch.Tensor, swiglu: bool = False, codes: Optional[torch.Te
                  scales: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """int8 codes [R, K] and fp32 scales [R] of the rows of x [R, K] (bfloat16 or
     float16), or of silu(gate) * up with x [R, 2 K] = gate | up where `swiglu`.
-    value = code * scale; a row with an infinity or NaN gets the scale NaN."""
+    value = code * scale; a row with an infinity or NaN gets the scale NaN.
+    Not differentiable: operands that need a gradient are refused."""
+    _no_gradient("moe_quant_i8", x, scales)
     (R, width), dev = _rows_of("x", x), x.device
     if swiglu and width % 2:
         raise ValueError(f"x: {width} columns do not split into gate and up")
@@ -645,7 +661,9 @@ def moe_mm_i8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Te
     [E, N] and offsets int32 [E + 1]; with row_token int32 [R] (moe_permute's)
     row r of the result takes row t = row_token[r] of xq, else t = r.
     The result [R, N] is bfloat16 (default), float16 or float32; rows of no
-    group are zeros in a new result and stay as they are in a caller's `out`."""
+    group are zeros in a new result and stay as they are in a caller's `out`.
+    Not differentiable: operands that need a gradient are refused."""
+    _no_gradient("moe_mm_i8", xs, ws, out)
     (T, width), dev = _rows_of("xq", xq), xq.device
     E, N, K, pw, pws, po = _i8_weights(wq, ws, offsets, dev)
     pq = _addr("xq", xq, (torch.int8,), (T, K), dev)
@@ -679,7 +697,9 @@ def moe_linear_i8(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets: 
     """moe_mm_i8 of moe_quant_i8(x, swiglu): 16-bit activations (bfloat16 or
     float16) times int8 weights.  The result has x's type unless out_dtype or
     `out` says otherwise.  `work`: uint8 scratch of at least
-    moe_linear_i8_workspace_size(...) bytes, allocated where absent and needed."""
+    moe_linear_i8_workspace_size(...) bytes, allocated where absent and needed.
+    Not differentiable: operands that need a gradient are refused."""
+    _no_gradient("moe_linear_i8", x, ws, out)
     (T, _), dev = _rows_of("x", x), x.device
     E, N, K, pw, pws, po = _i8_weights(wq, ws, offsets, dev)
     px = _addr("x", x, _16BIT, (T, 2 * K if swiglu else K), dev)
