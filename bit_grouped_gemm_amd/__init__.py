@@ -37,6 +37,7 @@ import os
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libmoe.so")
@@ -438,9 +439,19 @@ def _addr(name: str, t: torch.Tensor, dtypes, shape, dev: torch.device):
     return _ptr(t)
 
 
+def _no_tangent(name: str, *tensors: Optional[torch.Tensor]) -> None:
+    """Refuses operands (and outputs) with a forward-mode tangent, which the
+    result would be without (also under torch.no_grad(), which leaves forward mode on)."""
+    if getattr(forward_ad, "_current_level", 0) >= 0:  # inside a dual level
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError(f"{name} has no forward-mode derivative: give it operands without a tangent")
+
+
 def _no_gradient(name: str, *tensors: Optional[torch.Tensor]) -> None:
-    """Refuses operands (and outputs) that need a gradient: the result would be
-    cut from their graph without a word."""
+    """Refuses operands (and outputs) that need a gradient or carry a tangent: the
+    result would be cut from their graph without a word."""
+    _no_tangent(name, *tensors)
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
@@ -596,12 +607,15 @@ def moe_grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out:
     `out_dtype`): the gradients are moe_grouped_mm_dgrad and
     moe_grouped_mm_wgrad, and rows of no group get the gradient 0.  In a graph,
     capture forward and backward together, while no earlier result computed from
-    the same leaves is kept: PyTorch ties a leaf's gradient to the stream of its first use."""
+    the same leaves is kept: PyTorch ties a leaf's gradient to the stream of its first use.
+    Operands with a forward-mode tangent are refused."""
+    _no_tangent("moe_grouped_mm", x, w, out)
     if (x.requires_grad or w.requires_grad) and torch.is_grad_enabled():
         if out is not None or out_dtype not in (None, x.dtype):
             raise ValueError("moe_grouped_mm: out and out_dtype cannot be given where a gradient is needed")
         return _GroupedMM.apply(x, w, offsets)
-    _no_gradient("moe_grouped_mm with out", out)
+    if out is not None:
+        _no_gradient("moe_grouped_mm with out", out)
     return _grouped_mm(x, w, offsets, out, out_dtype)
 
 

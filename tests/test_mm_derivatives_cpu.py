@@ -2,6 +2,7 @@
 give: refused before any pointer is taken, so no GPU is needed."""
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 import bit_grouped_gemm_amd as moe
 
@@ -39,3 +40,26 @@ def test_an_operand_that_needs_a_gradient_is_refused(name, which):
     # where no graph is built, the call goes on to its other checks (these tensors are no GPU's)
     with torch.no_grad(), pytest.raises(ValueError, match="must live on the GPU"):
         CALLS[name][0](a)
+
+
+@pytest.mark.parametrize("name,which", EACH + [("moe_grouped_mm", "x"), ("moe_grouped_mm", "w")])
+def test_an_operand_with_a_tangent_is_refused(name, which):
+    """A dual tensor does not say that it needs a gradient; no_grad leaves forward mode on."""
+    a = operands()
+    with forward_ad.dual_level():
+        a[which] = forward_ad.make_dual(a[which], torch.ones_like(a[which]))
+        assert not a[which].requires_grad
+        for mode in (torch.enable_grad(), torch.no_grad()):
+            with mode, pytest.raises(ValueError, match="no forward-mode derivative"):
+                CALLS[name][0](a)
+    # a level without a tangent is no reason to refuse
+    with forward_ad.dual_level(), pytest.raises(ValueError, match="must live on the GPU"):
+        CALLS[name][0](operands())
+
+
+def test_a_differentiable_operand_with_a_tangent_is_refused():
+    a = operands()
+    with forward_ad.dual_level():
+        x = forward_ad.make_dual(a["x"].requires_grad_(), torch.ones_like(a["x"]))
+        with pytest.raises(ValueError, match="no forward-mode derivative"):
+            moe.moe_grouped_mm(x, a["w"], a["off"])
