@@ -468,6 +468,14 @@ def _new_or_checked(out, shape, dtype, allowed, like):
     return like.new_empty(shape, dtype=dtype), 1
 
 
+def _written(*given: Optional[torch.Tensor]) -> None:
+    """Tells autograd that a call wrote into a caller's tensors, so that a backward
+    pass which saved one of them raises instead of using the new values."""
+    for t in given:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 def _matrices(w: torch.Tensor):
     if w.dim() != 3:
         raise ValueError(f"w: shape {tuple(w.shape)}, expected (E, N, K)")
@@ -494,10 +502,12 @@ def _grouped(name, rows, p, w, offsets, width, other, out, out_dtype):
     po = _addr("offsets", offsets, (torch.int32,), (E + 1,), dev)
     if out is not None and out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
+    given = out
     out, clear = _new_or_checked(out, (R, other), out_dtype or dt, allowed, p)
     py = _addr("out", out, allowed, (R, other), dev)
     c = MoeMmCfg(R, N, K, E, 0, _DT[dt], _DT[out.dtype], clear)
     _call(name, dev.index, C.byref(c), pp, pw, po, py)
+    _written(given)
     return out
 
 
@@ -536,6 +546,7 @@ def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     po = _addr("offsets", offsets, (torch.int32,), (E + 1,), dev)
     if out is not None and out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
+    given = out
     out, _ = _new_or_checked(out, (E, N, K), out_dtype or dt, allowed, x)
     pw = _addr("out", out, allowed, (E, N, K), dev)
     c = MoeMmCfg(R, N, K, E, 0, _DT[dt], _DT[out.dtype], 0)
@@ -544,6 +555,7 @@ def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
         work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     pk = None if work is None else _addr("work", work, (torch.uint8,), work.shape, dev)
     _call("moe_grouped_mm_wgrad", dev.index, C.byref(c), pd, px, po, pw, pk, 0 if work is None else work.numel())
+    _written(given)
     return out
 
 
@@ -631,6 +643,7 @@ def moe_quant_i8(x: torch.Tensor, swiglu: bool = False, codes: Optional[torch.Te
         raise ValueError(f"x: {width} columns do not split into gate and up")
     K = width // 2 if swiglu else width
     px = _addr("x", x, _16BIT, (R, width), dev)
+    given = codes, scales
     if codes is None:
         codes = torch.empty(R, K, dtype=torch.int8, device=dev)
     if scales is None:
@@ -638,6 +651,7 @@ def moe_quant_i8(x: torch.Tensor, swiglu: bool = False, codes: Optional[torch.Te
     pq = _addr("codes", codes, (torch.int8,), (R, K), dev)
     ps = _addr("scales", scales, (torch.float32,), (R,), dev)
     _call("moe_quant_i8", dev.index, R, K, _DT[x.dtype], int(bool(swiglu)), px, pq, ps)
+    _written(*given)
     return codes, scales
 
 
@@ -685,10 +699,12 @@ def moe_mm_i8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Te
     R, pt = _row_token(row_token, T, dev)
     if out is not None and out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
+    given = out
     out, clear = _new_or_checked(out, (R, N), out_dtype or torch.bfloat16, tuple(_DT), xq)
     py = _addr("out", out, tuple(_DT), (R, N), dev)
     c = MoeMmCfg(R, N, K, E, T, 0, _DT[out.dtype], clear)
     _call("moe_mm_i8", dev.index, C.byref(c), pq, ps, pw, pws, po, pt, py)
+    _written(given)
     return out
 
 
@@ -720,6 +736,7 @@ def moe_linear_i8(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets: 
     R, pt = _row_token(row_token, T, dev)
     if out is not None and out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
+    given = out
     out, clear = _new_or_checked(out, (R, N), out_dtype or x.dtype, tuple(_DT), x)
     py = _addr("out", out, tuple(_DT), (R, N), dev)
     c = MoeMmCfg(R, N, K, E, T, _DT[x.dtype], _DT[out.dtype], clear)
@@ -729,6 +746,7 @@ def moe_linear_i8(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets: 
     pk = None if work is None else _addr("work", work, (torch.uint8,), work.shape, dev)
     _call("moe_linear_i8", dev.index, C.byref(c), px, int(bool(swiglu)), pw, pws, po, pt, py, pk,
           0 if work is None else work.numel())
+    _written(given)
     return out
 
 
