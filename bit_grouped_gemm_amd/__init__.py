@@ -439,23 +439,25 @@ def _addr(name: str, t: torch.Tensor, dtypes, shape, dev: torch.device):
     return _ptr(t)
 
 
-def _no_tangent(name: str, *tensors: Optional[torch.Tensor]) -> None:
-    """Refuses operands (and outputs) with a forward-mode tangent, which the
-    result would be without (also under torch.no_grad(), which leaves forward mode on)."""
-    if getattr(forward_ad, "_current_level", 0) >= 0:  # inside a dual level
-        for t in tensors:
-            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
-                raise ValueError(f"{name} has no forward-mode derivative: give it operands without a tangent")
+_grad_enabled = torch.is_grad_enabled
 
 
-def _no_gradient(name: str, *tensors: Optional[torch.Tensor]) -> None:
-    """Refuses operands (and outputs) that need a gradient or carry a tangent: the
-    result would be cut from their graph without a word."""
-    _no_tangent(name, *tensors)
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                raise ValueError(f"{name} has no gradient: call it under torch.no_grad() or detach its operands")
+def _refuse_derivatives(name: str, out: Optional[torch.Tensor], a: Optional[torch.Tensor] = None,
+                        b: Optional[torch.Tensor] = None) -> None:
+    """Refuses operands (and outputs) that need a gradient or carry a forward-mode
+    tangent, of which the result would be cut off without a word."""
+    if _grad_enabled() and (a is not None and a.requires_grad or b is not None and b.requires_grad
+                            or out is not None and out.requires_grad):
+        raise ValueError(f"{name} has no gradient: call it under torch.no_grad() or detach its operands")
+    if forward_ad._current_level >= 0:  # in a dual level
+        _refuse_tangents(name, out, a, b)
+
+
+def _refuse_tangents(name: str, *tensors: Optional[torch.Tensor]) -> None:
+    """The same for tangents alone: a dual tensor does not say that it needs a
+    gradient, and torch.no_grad() leaves forward mode on."""
+    if any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise ValueError(f"{name} has no forward-mode derivative: give it operands without a tangent")
 
 
 def _new_or_checked(out, shape, dtype, allowed, like):
@@ -468,12 +470,9 @@ def _new_or_checked(out, shape, dtype, allowed, like):
     return like.new_empty(shape, dtype=dtype), 1
 
 
-def _written(*given: Optional[torch.Tensor]) -> None:
-    """Tells autograd that a call wrote into a caller's tensors, so that a backward
-    pass which saved one of them raises instead of using the new values."""
-    for t in given:
-        if t is not None:
-            torch.autograd.graph.increment_version(t)
+# Tells autograd that a call wrote into a caller's tensor, so that a backward pass
+# which saved it raises instead of using the new values.
+_written = torch.autograd.graph.increment_version
 
 
 def _matrices(w: torch.Tensor):
@@ -507,7 +506,8 @@ def _grouped(name, rows, p, w, offsets, width, other, out, out_dtype):
     py = _addr("out", out, allowed, (R, other), dev)
     c = MoeMmCfg(R, N, K, E, 0, _DT[dt], _DT[out.dtype], clear)
     _call(name, dev.index, C.byref(c), pp, pw, po, py)
-    _written(given)
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -521,7 +521,7 @@ def moe_grouped_mm_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tenso
     """dx [R, K] = dy[r] @ w[e] for the rows r of each group e: moe_grouped_mm's
     gradient with respect to x.  `out` and `out_dtype` as in moe_grouped_mm.
     Not differentiable: operands that need a gradient are refused."""
-    _no_gradient("moe_grouped_mm_dgrad", dy, w, out)
+    _refuse_derivatives("moe_grouped_mm_dgrad", out, dy, w)
     _, N, K = _matrices(w)
     return _grouped("moe_grouped_mm_dgrad", "dy", dy, w, offsets, N, K, out, out_dtype)
 
@@ -535,7 +535,7 @@ def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     `work`: uint8 scratch of at least moe_grouped_mm_wgrad_workspace_size(...)
     bytes, allocated where absent and needed.  Not differentiable: operands that
     need a gradient are refused."""
-    _no_gradient("moe_grouped_mm_wgrad", dy, x, out)
+    _refuse_derivatives("moe_grouped_mm_wgrad", out, dy, x)
     (R, N), K, dt, dev = _rows_of("dy", dy), _rows_of("x", x)[1], dy.dtype, dy.device
     if offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError(f"offsets: shape {tuple(offsets.shape)}, expected (E + 1,)")
@@ -555,7 +555,8 @@ def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
         work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     pk = None if work is None else _addr("work", work, (torch.uint8,), work.shape, dev)
     _call("moe_grouped_mm_wgrad", dev.index, C.byref(c), pd, px, po, pw, pk, 0 if work is None else work.numel())
-    _written(given)
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -621,13 +622,14 @@ def moe_grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out:
     capture forward and backward together, while no earlier result computed from
     the same leaves is kept: PyTorch ties a leaf's gradient to the stream of its first use.
     Operands with a forward-mode tangent are refused."""
-    _no_tangent("moe_grouped_mm", x, w, out)
-    if (x.requires_grad or w.requires_grad) and torch.is_grad_enabled():
+    if forward_ad._current_level >= 0:
+        _refuse_tangents("moe_grouped_mm", x, w, out)
+    if (x.requires_grad or w.requires_grad) and _grad_enabled():
         if out is not None or out_dtype not in (None, x.dtype):
             raise ValueError("moe_grouped_mm: out and out_dtype cannot be given where a gradient is needed")
         return _GroupedMM.apply(x, w, offsets)
     if out is not None:
-        _no_gradient("moe_grouped_mm with out", out)
+        _refuse_derivatives("moe_grouped_mm with out", out)
     return _grouped_mm(x, w, offsets, out, out_dtype)
 
 
@@ -637,7 +639,7 @@ def moe_quant_i8(x: torch.Tensor, swiglu: bool = False, codes: Optional[torch.Te
     float16), or of silu(gate) * up with x [R, 2 K] = gate | up where `swiglu`.
     value = code * scale; a row with an infinity or NaN gets the scale NaN.
     Not differentiable: operands that need a gradient are refused."""
-    _no_gradient("moe_quant_i8", x, scales)
+    _refuse_derivatives("moe_quant_i8", scales, x)
     (R, width), dev = _rows_of("x", x), x.device
     if swiglu and width % 2:
         raise ValueError(f"x: {width} columns do not split into gate and up")
@@ -651,7 +653,9 @@ def moe_quant_i8(x: torch.Tensor, swiglu: bool = False, codes: Optional[torch.Te
     pq = _addr("codes", codes, (torch.int8,), (R, K), dev)
     ps = _addr("scales", scales, (torch.float32,), (R,), dev)
     _call("moe_quant_i8", dev.index, R, K, _DT[x.dtype], int(bool(swiglu)), px, pq, ps)
-    _written(*given)
+    for t in given:
+        if t is not None:
+            _written(t)
     return codes, scales
 
 
@@ -691,7 +695,7 @@ def moe_mm_i8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Te
     The result [R, N] is bfloat16 (default), float16 or float32; rows of no
     group are zeros in a new result and stay as they are in a caller's `out`.
     Not differentiable: operands that need a gradient are refused."""
-    _no_gradient("moe_mm_i8", xs, ws, out)
+    _refuse_derivatives("moe_mm_i8", out, xs, ws)
     (T, width), dev = _rows_of("xq", xq), xq.device
     E, N, K, pw, pws, po = _i8_weights(wq, ws, offsets, dev)
     pq = _addr("xq", xq, (torch.int8,), (T, K), dev)
@@ -704,7 +708,8 @@ def moe_mm_i8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Te
     py = _addr("out", out, tuple(_DT), (R, N), dev)
     c = MoeMmCfg(R, N, K, E, T, 0, _DT[out.dtype], clear)
     _call("moe_mm_i8", dev.index, C.byref(c), pq, ps, pw, pws, po, pt, py)
-    _written(given)
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -729,7 +734,7 @@ def moe_linear_i8(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets: 
     `out` says otherwise.  `work`: uint8 scratch of at least
     moe_linear_i8_workspace_size(...) bytes, allocated where absent and needed.
     Not differentiable: operands that need a gradient are refused."""
-    _no_gradient("moe_linear_i8", x, ws, out)
+    _refuse_derivatives("moe_linear_i8", out, x, ws)
     (T, _), dev = _rows_of("x", x), x.device
     E, N, K, pw, pws, po = _i8_weights(wq, ws, offsets, dev)
     px = _addr("x", x, _16BIT, (T, 2 * K if swiglu else K), dev)
@@ -746,7 +751,8 @@ def moe_linear_i8(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets: 
     pk = None if work is None else _addr("work", work, (torch.uint8,), work.shape, dev)
     _call("moe_linear_i8", dev.index, C.byref(c), px, int(bool(swiglu)), pw, pws, po, pt, py, pk,
           0 if work is None else work.numel())
-    _written(given)
+    if given is not None:
+        _written(given)
     return out
 
 
