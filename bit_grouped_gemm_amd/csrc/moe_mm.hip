@@ -927,9 +927,12 @@ bool plan(int op, const MmArgs& a, TileShape* s, long* grid) {
 
 // Rows of a dense product's first launch.  Where the last few rows would make
 // the large tiles go one more round, they go into a launch of their own, in the
-// shape that suits them (int8, 4099 rows, K = 7168, N = 4096, quantised: 180 us in
-// one launch, 121 in two); a launch counts as much as bringing in kLaunchBytes.
-constexpr double kLaunchBytes = 150e3;
+// shape that suits them; a launch counts as much as bringing in kLaunchBytes.
+// (int8, N = 4096, us in one launch and in two, by the bytes that two save, in KB: 4099
+// rows, K = 7168, 3441: 159 and 100; 2051, 7168, 688: 77 and 61; 2051, 4096, 393: 50 and
+// 41; 300, 4096, 262: 20 and 16; 1030, 7168, 229: 44 and 68; 523, 7168, 229: 48 and
+// 46; 1030, 4096, 131: 29 and 42; 523, 1024, 33: 10 and 16.)
+constexpr double kLaunchBytes = 250e3;
 int first_rows(int op, const MmArgs& a) {
   if (op != kFwd || a.offsets || a.R <= 256) return a.R;
   double one, head, tail;

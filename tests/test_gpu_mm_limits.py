@@ -129,3 +129,24 @@ def test_offsets_that_name_rows_many_times_stay_inside_the_tensors(E, R):
     assert all_equal(flat[:margin], 5) and all_equal(flat[margin + R:], 5)
     # zeros times weights, or left alone
     assert all(bool(((p == 0) | (p == 5)).all()) for p in flat.reshape(-1).split(1 << 30))
+
+
+# ------------------------------------------------------------------ one launch or two
+@pytest.mark.parametrize("K", [1024, 7168])
+@pytest.mark.parametrize("R", [256, 257, 300, 523, 1030, 2051, 4096, 4101])
+def test_mm_i8_dense_in_one_launch_or_two(R, K):
+    """Row counts on both sides of the rule that gives the last rows a launch of
+    their own: each row comes out as it does alone, whichever it is."""
+    g = gen(8)
+    N = 4096
+    xq, xs = codes(g, R, K), torch.rand(R, device=DEV, generator=g) * 1e-2
+    wq, ws = codes(g, N, K), torch.rand(N, device=DEV, generator=g) * 1e-3
+    y = torch.full((R, N), 7.0, dtype=FP32, device=DEV)
+    moe.moe_mm_i8(xq, xs, wq, ws, out=y)
+    t = torch.arange(R, dtype=torch.int32, device=DEV)
+    assert torch.equal(y, moe.moe_mm_i8(xq, xs, wq, ws, row_token=t, out_dtype=FP32))
+    for a in (0, R // 256 * 256 - 5, R - 5):  # the first rows, those around the border, the last
+        a = max(a, 0)
+        some = xq[a:a + 10].contiguous(), xs[a:a + 10].clone()
+        assert torch.equal(y[a:a + 10], moe.moe_mm_i8(*some, wq, ws, out_dtype=FP32))
+    near_i8(y, xq.double() @ wq.double().t() * xs.double()[:, None] * ws.double(), "y")
