@@ -587,10 +587,19 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
 // a ring of S stages of its own, so nothing waits for another wave until the
 // sums are added up, in the order of the waves, through LDS.  Bound by the
 // weights' bytes and their latency: S - 1 steps of 2 KB per 16 columns are in
-// flight per wave, on every CU.  S is what lets two workgroups share a CU where
-// that pays (16 x 64 tiles: S = 2 and two of them 131 us, S = 4 and one 177; 61
-// tokens, top-8 of 64, 1536 -> 4096).  One bf16 token through 8 of 64 experts,
-// 4096 -> 1536: 18 us, 5.6 TB/s of weights; a copy reaches 4.8 TB/s on this card.
+// flight per wave, on every CU.  One bf16 token through 8 of 64 experts, 4096 ->
+// 1536: 18 us, 5.4 TB/s of weights; a stream of plain reads reaches 6.9 TB/s.
+//
+// S is 2, which lets the most workgroups share a CU's LDS.  With 2, 3 and 4
+// stages, us, cold weights: 16 x 64 tiles (61 tokens, top-8 of 64, 1536 -> 4096) 130,
+// 161, 174; 16 x 32 (6 matrices of 4096 x 4096, one int8 row each) 18, 20, 23; 32 x
+// 16 (20000 rows in 8 groups, 4096 -> 16) 27, 28, 31; 32 x 32 (61 rows, 4096 -> 4096)
+// 12.5, 13.9, 13.6; 32 x 64 (192 rows in 16 groups, 4096 -> 2048) 46, 48; 64 x 16 (612
+// rows, 4096 -> 400) 13.0, 14.1, 13.7; 64 x 32 (1800 rows in 4 groups, 2048 -> 520)
+// 24.2, 26.0.  16 x 16 tiles have four: as a rule they are what products of up to
+// one tile per CU get, where nothing shares a CU and a deep ring hides the loads'
+// latency (one row, 7168 -> 4096: 14.6, 12.1, 11.7; 8 groups of a row, three
+// tiles per CU: 17.9, 18.4, 19.1).
 constexpr int kFewWaves = 4;
 
 template <int TY, int NC, int NT, int S>
@@ -602,9 +611,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_mm_few(MmArgs a) {
   // one array per stage: see k_mm
   __shared__ __align__(1024) uint8_t st0[kFewWaves * kStage];
   __shared__ __align__(1024) uint8_t st1[kFewWaves * kStage];
-  __shared__ __align__(1024) uint8_t st2[S >= 3 ? kFewWaves * kStage : 16];
-  __shared__ __align__(1024) uint8_t st3[S >= 4 ? kFewWaves * kStage : 16];
-  static_assert(S >= 2 && S <= 4 && (S - 1) * L < 64, "ring");
+  __shared__ __align__(1024) uint8_t st2[S == 4 ? kFewWaves * kStage : 16];
+  __shared__ __align__(1024) uint8_t st3[S == 4 ? kFewWaves * kStage : 16];
+  static_assert((S == 2 || S == 4) && (S - 1) * L < 64, "ring");
   static_assert(NC * NT * 1024 <= kStage, "a wave's sums fit a stage");
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, g = lane >> 4;
@@ -681,16 +690,14 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_mm_few(MmArgs a) {
     __builtin_amdgcn_sched_barrier(0);
   };
   issue(st0, 0);
-  if (S >= 3) issue(st1, 1);
-  if (S >= 4) issue(st2, 2);
+  if constexpr (S == 4) {
+    issue(st1, 1);
+    issue(st2, 2);
+  }
   for (int k = 0; k < mine; k += S) {
     if constexpr (S == 2) {
       issue(st1, k + 1); multiply(st0);
       issue(st0, k + 2); multiply(st1);
-    } else if constexpr (S == 3) {
-      issue(st2, k + 2); multiply(st0);
-      issue(st0, k + 3); multiply(st1);
-      issue(st1, k + 4); multiply(st2);
     } else {
       issue(st3, k + 3); multiply(st0);
       issue(st0, k + 4); multiply(st1);
@@ -993,12 +1000,12 @@ static hipError_t launch_shape(const MmArgs& a, const TileShape& s, unsigned gri
   } else {
     if constexpr (OP == kFwd) {
       if (s.few) {
-#define MOE_FEW(NT, NC, S) \
-  case NT * 16 + NC: MOE_MM((k_mm_few<TY, NC, NT, S>), kFewWaves * 64); break;
+#define MOE_FEW(NT, NC) \
+  case NT * 16 + NC: MOE_MM((k_mm_few<TY, NC, NT, NT * NC == 1 ? 4 : 2>), kFewWaves * 64); break;
         switch (s.rows + s.cols / 16) {
-          MOE_FEW(1, 1, 4) MOE_FEW(1, 2, 3) MOE_FEW(1, 4, 2)
-          MOE_FEW(2, 1, 4) MOE_FEW(2, 2, 2) MOE_FEW(2, 4, 2)
-          MOE_FEW(4, 1, 2) MOE_FEW(4, 2, 3) MOE_FEW(4, 4, 2)
+          MOE_FEW(1, 1) MOE_FEW(1, 2) MOE_FEW(1, 4)
+          MOE_FEW(2, 1) MOE_FEW(2, 2) MOE_FEW(2, 4)
+          MOE_FEW(4, 1) MOE_FEW(4, 2) MOE_FEW(4, 4)
         }
 #undef MOE_FEW
         return hipGetLastError();
