@@ -976,12 +976,14 @@ size_t wgrad_bytes(const MmArgs& a) {
 // workgroup per tile.  Turns hide a tile's first loads and its stores, which
 // counts where reductions are short; but they cost the third stage, the last
 // round's empty places cost their whole length, and long groups are not evened out.
+// places: the launch's workgroups, as one per tile: the tiles and the empty
+// places behind the last of each XCD.
 // (Cold operands, us, turns and one per tile: 64 groups, 1408 x 2048, 12 tiles per CU,
 // of 16 rows 87 and 98, 128 116 and 123, 256 186 and 175, 1024 422 and 403; 256 groups,
 // 512 x 512, of 128 51 and 55, 192 75 and 69; 16 groups, 4096 x 2048, of 128 79 and 86, 1024
 // 311 and 267; 64 groups, 768 x 768, 2.25 per CU, of 128 33 and 34, 512 82 and 61.)
-static bool takes_turns(const MmArgs& a, long tiles) {
-  const double rows = double(a.R) / (double(a.E) * a.splits), each = tiles / kCUs;
+static bool takes_turns(const MmArgs& a, long places) {
+  const double rows = double(a.R) / (double(a.E) * a.splits), each = places / kCUs;
   return each > 1 && rows <= 128 && rows * (std::ceil(each) / each - 1) < 64;
 }
 
