@@ -310,10 +310,10 @@ __global__ __launch_bounds__(kThreads) void k_mm(MmArgs a) {
   using QS = Stream<QT, kBN>;
   // Stages: as many as the CU's LDS holds (two workgroups of BM = 64 share it).
   // Each is needed a step later than its loads go out, so a third one gives
-  // loads that miss the L2 two steps' time.  (Ragged groups, 32768 rows, 4096
-  // -> 1536, E=64: two stages of both 482 us, a third of q 435; 2048 -> 1408:
-  // dx 157 against 133; dW of 16 groups of 1024, 2048 -> 4096, cold operands, 302 against 285;
-  // nothing where all is in the L2.)
+  // loads that miss the L2 two steps' time.  (Cold operands, us, two stages of both and
+  // these: ragged groups, 32768 rows, 4096 -> 1536, E=64, forward 470 and 435, dx 484 and
+  // 456; 12248 rows, 2048 -> 1408, E=64, forward 123 and 117, dx 158 and 129; dW of 16
+  // groups of 1024, 2048 -> 4096, 299 and 266 to 279; nothing where all is in the L2.)
   // kTurns: a workgroup takes several tiles of dW in turn, and the next one's first
   // stages load while one is stored from pieces of LDS of its own, which take
   // the third stage's place (see takes_turns).
@@ -979,9 +979,9 @@ size_t wgrad_bytes(const MmArgs& a) {
 // places: the launch's workgroups, as one per tile: the tiles and the empty
 // places behind the last of each XCD.
 // (Cold operands, us, turns and one per tile: 64 groups, 1408 x 2048, 12 tiles per CU,
-// of 16 rows 87 and 98, 128 116 and 123, 256 186 and 175, 1024 422 and 403; 256 groups,
-// 512 x 512, of 128 51 and 55, 192 75 and 69; 16 groups, 4096 x 2048, of 128 79 and 86, 1024
-// 311 and 267; 64 groups, 768 x 768, 2.25 per CU, of 128 33 and 34, 512 82 and 61.)
+// of 16 rows 79 and 91, 128 105 and 113, 256 144 and 152, 1024 410 and 384; 256 groups,
+// 512 x 512, of 128 47 and 48, 192 63 and 60; 16 groups, 4096 x 2048, of 128 77 and 82, 1024
+// 300 and 266; 64 groups, 768 x 768, 2.25 per CU, of 128 32 and 31, 512 66 and 64.)
 static bool takes_turns(const MmArgs& a, long places) {
   const double rows = double(a.R) / (double(a.E) * a.splits), each = places / kCUs;
   return each > 1 && rows <= 128 && rows * (std::ceil(each) / each - 1) < 64;

@@ -4,7 +4,8 @@
 // One pass over the data: a row's values stay in registers between the
 // maximum and the rounding (rows of up to 16384 values; longer ones are read
 // again, from L2 as a rule).  Bound by HBM: 2 (SwiGLU: 4) bytes in and one out
-// per value; 32768 rows of 7168: 127 us, 5.5 TB/s.
+// per value; 32768 rows of 7168: 127 us, 5.5 TB/s; SwiGLU of 32768 rows of 2048: 77
+// us, 4.4 TB/s.
 #include "moe_quant_i8.h"
 
 namespace moe {
