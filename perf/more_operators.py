@@ -233,7 +233,7 @@ def _plain_quant(v):
     top = blocks.abs().amax(dim=2)
     exponent = (torch.frexp(top).exponent - 3).clamp(-127, 127)
     exponent = torch.where(top == 0, -127, exponent)
-    u = torch.ldexp(blocks, -exponent[:, :, None])
+    u = blocks * torch.exp2(-exponent.float())[:, :, None]  # (ldexp's powers are not exact on a GPU)
     a = u.abs()
     # steps of 1/2 below 2, of 1 below 4, of 2 above; ties to even
     step = torch.where(a < 2, 0.5, torch.where(a < 4, 1.0, 2.0))
@@ -278,8 +278,8 @@ def _plain_linear(s):
         gate, up = v.chunk(2, dim=1)
         v = gate / (1 + torch.exp(-gate)) * up
     u, exponent = _plain_quant(v)
-    return _plain_product(s, torch.ldexp(u.view(*exponent.shape, 32), exponent[:, :, None]).view(u.shape),
-                          s["x"].dtype)
+    x = u.view(*exponent.shape, 32) * torch.exp2(exponent.float())[:, :, None]
+    return _plain_product(s, x.view(u.shape), s["x"].dtype)
 
 
 def _plain_mm(s):
