@@ -24,6 +24,9 @@ and on row-major weights (nothing to prepack):
     moe_quant_i8(x, swiglu=False) -> (codes, scales)   (int8, one scale per token)
     moe_mm_i8(xq, xs, wq, ws, offsets=None, row_token=None) -> y   (grouped or dense)
     moe_linear_i8(x, wq, ws, offsets=None, row_token=None, swiglu=False) -> y   (both in one call)
+and in front of them
+    moe_rms_norm(x, weight, residual=None) -> y, or (y, x + residual)   (differentiable)
+    moe_rms_norm_quant(x, weight, residual=None, fmt=QFMT_E4M3) -> (codes, scales, y, sum)
 
 The layer's GEMM entry points read expert weights in the tiled layout: convert the
 canonical row-major tensors once with moe_prepack_weights(cfg, weights)
@@ -53,6 +56,9 @@ MOE_ERR_HIP = 6
 WFMT_FP8_BLOCK = 0
 WFMT_MXFP4 = 1
 WFMT_NVFP4 = 2
+QFMT_E4M3 = 0  # moe_rms_norm_quant's codes
+QFMT_I8 = 1
+QFMT_MXFP4 = 2
 RATE_E2M1_E2M1 = 16  # moe_mfma_rate's e2m1 x e2m1 operand pair
 
 EXPORTS = ("moe_workspace_size", "moe_permute", "moe_grouped_gemm1_swiglu", "moe_grouped_gemm2",
@@ -62,7 +68,8 @@ EXPORTS = ("moe_workspace_size", "moe_permute", "moe_grouped_gemm1_swiglu", "moe
            "moe_mfma_rate", "moe_encode_e4m3", "moe_route", "moe_route_workspace_size", "moe_status_str",
            "moe_grouped_mm", "moe_grouped_mm_dgrad", "moe_grouped_mm_wgrad",
            "moe_grouped_mm_wgrad_workspace_size", "moe_quant_i8", "moe_mm_i8",
-           "moe_linear_i8", "moe_linear_i8_workspace_size")
+           "moe_linear_i8", "moe_linear_i8_workspace_size",
+           "moe_rms_norm", "moe_rms_norm_quant", "moe_rms_norm_backward", "moe_rms_norm_backward_workspace_size")
 
 # element types of the row-major products
 _DT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
@@ -80,6 +87,10 @@ class MoeWeights(C.Structure):
 
 class MoeMmCfg(C.Structure):
     _fields_ = [(n, C.c_int32) for n in ("R", "N", "K", "E", "T", "dtype", "out_dtype", "clear_rest")]
+
+
+class MoeNormCfg(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("R", "K", "dtype", "weight_dtype", "fmt", "group")] + [("eps", C.c_float)]
 
 
 class MoeError(RuntimeError):
@@ -127,6 +138,11 @@ def load(path: str = LIB_PATH) -> C.CDLL:
     L.moe_mm_i8.argtypes = [mmp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.moe_linear_i8_workspace_size.argtypes = [mmp, C.c_int, C.POINTER(sz)]
     L.moe_linear_i8.argtypes = [mmp, vp, C.c_int, vp, vp, vp, vp, vp, vp, sz, vp]
+    normp = C.POINTER(MoeNormCfg)
+    L.moe_rms_norm.argtypes = [normp, vp, vp, vp, vp, vp, vp, vp]
+    L.moe_rms_norm_quant.argtypes = [normp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.moe_rms_norm_backward.argtypes = [normp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_rms_norm_backward_workspace_size.argtypes = [normp, C.POINTER(sz)]
     L.moe_status_str.argtypes = [C.c_int]
     L.moe_status_str.restype = C.c_char_p
     for n in EXPORTS:
@@ -754,6 +770,177 @@ def moe_linear_i8(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets: 
     if given is not None:
         _written(given)
     return out
+
+
+# ------------------------------------------------------------------ RMS norm
+def _norm_operands(x, weight, residual, eps, fmt=0, group=0):
+    """The call's cfg, sizes and the addresses of x, residual and weight."""
+    (R, K), dt, dev = _rows_of("x", x), x.dtype, x.device
+    px = _addr("x", x, _16BIT, (R, K), dev)
+    pr = None if residual is None else _addr("residual", residual, (dt,), (R, K), dev)
+    pw = _addr("weight", weight, (dt, torch.float32), (K,), dev)
+    return MoeNormCfg(R, K, _DT[dt], _DT[weight.dtype], fmt, group, eps), R, K, px, pr, pw
+
+
+def _beside(name, given, like):
+    """An output of the operand's own kind: a new one, or the caller's."""
+    out = torch.empty_like(like) if given is None else given
+    return out, _addr(name, out, (like.dtype,), like.shape, like.device)
+
+
+def _rms_norm(x, weight, residual, eps, out=None, sum_out=None, want_rstd=False):
+    c, R, K, px, pr, pw = _norm_operands(x, weight, residual, eps)
+    y, py = _beside("out", out, x)
+    s = ps = rstd = None
+    if residual is not None:
+        s, ps = _beside("sum_out", sum_out, x)
+        if R and py == ps:
+            raise ValueError("out and sum_out are the same tensor")
+    if want_rstd:
+        rstd = torch.empty(R, dtype=torch.float32, device=x.device)
+    _call("moe_rms_norm", x.device.index, C.byref(c), px, pr, pw, py, ps,
+          None if rstd is None else rstd.data_ptr() or None)
+    for t in (out, sum_out if residual is not None else None):
+        if t is not None:
+            _written(t)
+    return y, s, rstd
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        ctx.set_materialize_grads(False)
+        y, s, rstd = _rms_norm(x, weight, residual, eps, want_rstd=True)
+        ctx.eps, ctx.sums = eps, residual is not None
+        ctx.save_for_backward(s if ctx.sums else x, weight, rstd)
+        return (y, s) if ctx.sums else y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, ds=None):
+        s, weight, rstd = ctx.saved_tensors
+        need_x = ctx.needs_input_grad[0] or ctx.needs_input_grad[2]
+        need_w = ctx.needs_input_grad[1]
+        if dy is None:  # only the sum was used: its gradient is x's and the residual's
+            return ds if ctx.needs_input_grad[0] else None, None, ds if ctx.needs_input_grad[2] else None, None
+        dx = torch.empty_like(s) if need_x else None
+        dw = torch.empty_like(weight) if need_w else None
+        _rms_norm_backward(_usable(dy), None if ds is None else _usable(ds), s, rstd, weight, ctx.eps, dx, dw, None)
+        return dx if ctx.needs_input_grad[0] else None, dw, dx if ctx.needs_input_grad[2] else None, None
+
+
+def _usable(dy):
+    """A gradient as the kernels take it: autograd's may be an expanded or an unaligned view."""
+    dy = dy.contiguous()
+    return dy.clone() if dy.data_ptr() % 16 else dy
+
+
+def _norm_bytes(c: MoeNormCfg) -> int:
+    n = C.c_size_t(0)
+    _check("moe_rms_norm_backward_workspace_size",
+           (_lib or load()).moe_rms_norm_backward_workspace_size(C.byref(c), C.byref(n)))
+    return n.value
+
+
+def _rms_norm_backward(dy, dsum, s, rstd, weight, eps, dx, dw, work):
+    (R, K), dt, dev = _rows_of("dy", dy), dy.dtype, dy.device
+    pd = _addr("dy", dy, _16BIT, (R, K), dev)
+    pg = None if dsum is None else _addr("dsum", dsum, (dt,), (R, K), dev)
+    ps = _addr("sum", s, (dt,), (R, K), dev)
+    pr = _addr("rstd", rstd, (torch.float32,), (R,), dev)
+    pw = _addr("weight", weight, (dt, torch.float32), (K,), dev)
+    px = None if dx is None else _addr("dx", dx, (dt,), (R, K), dev)
+    pdw = None if dw is None else _addr("dweight", dw, (weight.dtype,), (K,), dev)
+    c = MoeNormCfg(R, K, _DT[dt], _DT[weight.dtype], 0, 0, eps)
+    if work is None and dw is not None:
+        need = _norm_bytes(c)
+        work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    pk = None if work is None else _addr("work", work, (torch.uint8,), work.shape, dev)
+    _call("moe_rms_norm_backward", dev.index, C.byref(c), pd, pg, ps, pr, pw, px, pdw, pk,
+          0 if work is None else work.numel())
+
+
+def moe_rms_norm_backward_workspace_size(R: int, K: int) -> int:
+    """Bytes of scratch moe_rms_norm_backward needs for the gradient of the weight."""
+    return _norm_bytes(MoeNormCfg(R, K, 0, 0, 0, 0, 1.0))
+
+
+def moe_rms_norm_backward(dy: torch.Tensor, dsum: Optional[torch.Tensor], sum: torch.Tensor, rstd: torch.Tensor,
+                          weight: torch.Tensor, eps: float = 1e-6,
+                          work: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(dx, dweight) of moe_rms_norm: `sum` [R, K] is what was normalised, `rstd`
+    float32 [R] is 1 / sqrt(mean(sum^2) + eps), `dsum` (or None) the gradient that
+    reaches the sum by itself.  dx is the residual's gradient too.  `work`: uint8
+    scratch of at least moe_rms_norm_backward_workspace_size(R, K) bytes,
+    allocated where absent.  Not differentiable: operands that need a gradient are refused."""
+    _refuse_derivatives("moe_rms_norm_backward", dsum, dy, sum)
+    _refuse_derivatives("moe_rms_norm_backward", None, rstd, weight)
+    dx, dw = torch.empty_like(sum), torch.empty_like(weight)
+    _rms_norm_backward(dy, dsum, sum, rstd, weight, eps, dx, dw, work)
+    return dx, dw
+
+
+def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 out: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None):
+    """y [R, K] = s / sqrt(mean(s^2) + eps) * weight for the rows of s = x +
+    residual; returns y, or (y, s) where there is a residual.
+
+    x and residual [R, K] are bfloat16 or float16 (K a multiple of 8 up to
+    16384), weight [K] is of their type or float32.  s is rounded to their type
+    before it is normalised: it is what the residual stream carries on.  `out` and
+    `sum_out` receive y and s; `sum_out` may be x or residual itself.  All tensors
+    are contiguous and on one GPU.
+
+    Differentiable with respect to x, weight and residual (once; not with `out`
+    or `sum_out`).  Operands with a forward-mode tangent are refused.  In a
+    graph, capture forward and backward together, while no earlier result computed
+    from the same leaves is kept."""
+    if forward_ad._current_level >= 0:
+        _refuse_tangents("moe_rms_norm", x, weight, residual, out, sum_out)
+    if _grad_enabled():
+        if x.requires_grad or weight.requires_grad or residual is not None and residual.requires_grad:
+            if out is not None or sum_out is not None:
+                raise ValueError("moe_rms_norm: out and sum_out cannot be given where a gradient is needed")
+            return _RmsNorm.apply(x, weight, residual, eps)
+        _refuse_derivatives("moe_rms_norm with out", out, sum_out)
+    y, s, _ = _rms_norm(x, weight, residual, eps, out, sum_out)
+    return y if residual is None else (y, s)
+
+
+def moe_rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                       eps: float = 1e-6, fmt: int = QFMT_E4M3, group: int = 128, want_y: bool = False,
+                       sum_out: Optional[torch.Tensor] = None):
+    """moe_rms_norm with quantised rows: (codes, scales, y, sum).
+
+    fmt QFMT_E4M3: codes uint8 [R, K] and float32 scales [R, K / group], group 32
+    or 128 (the layer's xq and xs: moe_grouped_gemm1_swiglu takes them); QFMT_I8:
+    int8 [R, K] and float32 [R] (moe_mm_i8's); QFMT_MXFP4: uint8 [R, K / 2] and
+    [R, K / 32] (moe_mm_mx4's).  y is the 16-bit result, for the router, or None
+    without `want_y`; sum is x + residual, or None without a residual.  `sum_out` may
+    be x or residual itself.  Not differentiable: operands that need a gradient are refused."""
+    _refuse_derivatives("moe_rms_norm_quant", residual, x, weight)
+    _refuse_derivatives("moe_rms_norm_quant", sum_out)
+    c, R, K, px, pr, pw = _norm_operands(x, weight, residual, eps, fmt, group)
+    dev = x.device
+    y = py = s = ps = None
+    if want_y:
+        y, py = _beside("y", None, x)
+    if residual is not None:
+        s, ps = _beside("sum_out", sum_out, x)
+    if fmt == QFMT_MXFP4:
+        codes = torch.empty(R, K // 2, dtype=torch.uint8, device=dev)
+        scales = torch.empty(R, K // 32, dtype=torch.uint8, device=dev)
+    elif fmt == QFMT_I8:
+        codes = torch.empty(R, K, dtype=torch.int8, device=dev)
+        scales = torch.empty(R, dtype=torch.float32, device=dev)
+    else:
+        codes = torch.empty(R, K, dtype=torch.uint8, device=dev)
+        scales = torch.empty(R, K // max(group, 1), dtype=torch.float32, device=dev)
+    _call("moe_rms_norm_quant", dev.index, C.byref(c), px, pr, pw, py, ps, codes.data_ptr() or None,
+          scales.data_ptr() or None)
+    if s is not None and sum_out is not None:
+        _written(sum_out)
+    return codes, scales, y, s
 
 
 def raw_call(name: str, *args) -> int:

@@ -1,11 +1,7 @@
 // moe_mm_api.hip -- the C ABI of the row-major products and the int8
 // quantiser declared in include/moe.h: argument checks and launches.  Host
 // code only; the kernels live in moe_mm.hip and moe_quant_i8.hip.
-#include <cstdint>
-#include <initializer_list>
-#include <utility>
-
-#include "../../include/moe.h"
+#include "moe_check.h"
 #include "moe_mm.h"
 
 using namespace moe;
@@ -13,27 +9,7 @@ using namespace moe;
 namespace {
 
 constexpr int kMaxDim = 1 << 20;   // N, K: a tile's rows stay inside a 32-bit byte range
-constexpr int kMaxRows = 0x7FFFFFFF - 1023;  // a row count rounded up to a tile stays an int32
 constexpr int kMaxKInt8 = 1 << 16;  // 128 * 128 * K stays inside an int32 sum
-
-size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
-int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
-
-// (pointer, required)
-using PtrList = std::initializer_list<std::pair<const void*, bool>>;
-int null_ptrs(PtrList ps) {
-  for (auto& p : ps)
-    if (p.second && !p.first) return MOE_ERR_NULL_ARG;
-  return MOE_OK;
-}
-// tensors on 16 bytes, index arrays (a slice of a longer one, say) on 4
-int misaligned_ptrs(std::initializer_list<const void*> tensors, std::initializer_list<const int32_t*> indices = {}) {
-  for (auto p : tensors)
-    if (reinterpret_cast<uintptr_t>(p) & 15u) return MOE_ERR_MISALIGNED;
-  for (auto p : indices)
-    if (reinterpret_cast<uintptr_t>(p) & 3u) return MOE_ERR_MISALIGNED;
-  return MOE_OK;
-}
 
 int check_dims(const moe_mm_cfg* c) {
   if (c->R < 0 || c->R > kMaxRows || c->N < 1 || c->K < 1 || c->E < 1 || c->E > 1024) return MOE_ERR_BAD_SHAPE;

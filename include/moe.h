@@ -420,6 +420,65 @@ int moe_linear_i8(const moe_mm_cfg* cfg, const void* x, int swiglu, const int8_t
                   const int32_t* offsets, const int32_t* row_token, void* y, void* work, size_t work_bytes,
                   void* stream);
 
+/* ------------------------------------------------------------------------
+ * Root-mean-square norm with the residual's addition, in front of the router
+ * and of the products: for each row
+ *   s = x + residual, rounded to the rows' type (without residual s = x),
+ *   rstd = 1 / sqrt(mean(s^2) + eps),  y = s * rstd * weight.
+ * All sums and y itself are fp32 until the one rounding of what is written.
+ *
+ * moe_norm_cfg (host struct):
+ *   R rows of K values (K a multiple of 8 up to 2^14; R up to 2^31 - 1024)
+ *   dtype of x, residual, sum and y (MOE_DT_BF16 / MOE_DT_FP16);
+ *   weight_dtype: that type or MOE_DT_FP32
+ *   fmt, group: the codes of moe_rms_norm_quant (not used by the others)
+ *   eps: 1e-30 .. 1
+ * sum may be x's or residual's own buffer, and so may y where sum is not; else
+ * no output overlaps an operand or another output.
+ * A row that holds an infinity or NaN follows the formula: with an infinity
+ * rstd = 0, its finite values give 0 and the infinity NaN; with a NaN all is NaN. */
+enum { MOE_QFMT_E4M3 = 0, MOE_QFMT_I8 = 1, MOE_QFMT_MXFP4 = 2 };
+typedef struct moe_norm_cfg {
+  int32_t R, K;
+  int32_t dtype;
+  int32_t weight_dtype;
+  int32_t fmt;
+  int32_t group;
+  float eps;
+} moe_norm_cfg;
+
+/*   x [R][K]; residual [R][K] or NULL; weight [K]; y [R][K]
+ *   sum [R][K] or NULL: s, written only where there is a residual
+ *   rstd fp32 [R] or NULL (what the backward pass takes) */
+int moe_rms_norm(const moe_norm_cfg* cfg, const void* x, const void* residual, const void* weight, void* y,
+                 void* sum, float* rstd, void* stream);
+
+/* The same with y's codes, made from the fp32 values:
+ *   MOE_QFMT_E4M3  codes uint8 [R][K], scales fp32 [R][K / group], group 32 or
+ *                  128, by the layer's activation rule: moe_permute's xq and xs
+ *   MOE_QFMT_I8    codes int8 [R][K], scales fp32 [R], by moe_quant_i8's rule
+ *                  (K a multiple of 16): what moe_mm_i8 takes
+ *   MOE_QFMT_MXFP4 codes uint8 [R][K / 2], scales uint8 [R][K / 32], by
+ *                  moe_quant_mx4's rule: what moe_mm_mx4 takes
+ *   A group (MOE_QFMT_I8: a row) that is not finite has codes 0 and the scale NaN.
+ *   y [R][K] or NULL: the 16-bit result beside the codes (for the router). */
+int moe_rms_norm_quant(const moe_norm_cfg* cfg, const void* x, const void* residual, const void* weight, void* y,
+                       void* sum, void* codes, void* scales, void* stream);
+
+/* The gradients of moe_rms_norm, with n = s * rstd and g = dy * weight:
+ *   dx = rstd * (g - n * mean(g * n)) + dsum     (x's and the residual's)
+ *   dweight = sum over rows of dy * n            (zeros for R = 0)
+ *   dy [R][K]; dsum [R][K] or NULL: the gradient that reaches s by itself
+ *   sum [R][K]: s (x where there was no residual); rstd of the forward call
+ *   dx [R][K] or NULL; dweight [K] of weight_dtype or NULL
+ *   work: device scratch of moe_rms_norm_backward_workspace_size(cfg) bytes
+ *   (contents on entry ignored; not needed without dweight).
+ * The sums' order depends on R and K alone: equal inputs give equal bits. */
+int moe_rms_norm_backward_workspace_size(const moe_norm_cfg* cfg, size_t* bytes);
+int moe_rms_norm_backward(const moe_norm_cfg* cfg, const void* dy, const void* dsum, const void* sum,
+                          const float* rstd, const void* weight, void* dx, void* dweight, void* work,
+                          size_t work_bytes, void* stream);
+
 /* Diagnostic: read `bytes` (a multiple of 16) of device memory at `buf`
  * once -- a plain HBM read stream, the achievable-bandwidth reference for
  * the weight-streaming GEMMs.  Four workgroups of four waves per CU; each
