@@ -24,6 +24,7 @@ and on row-major weights (nothing to prepack):
     moe_quant_i8(x, swiglu=False) -> (codes, scales)   (int8, one scale per token)
     moe_mm_i8(xq, xs, wq, ws, offsets=None, row_token=None) -> y   (grouped or dense)
     moe_linear_i8(x, wq, ws, offsets=None, row_token=None, swiglu=False) -> y   (both in one call)
+    moe_quant_mx4, moe_mm_mx4, moe_linear_mx4   (the same three in MXFP4: e2m1 codes, an e8m0 scale per 32)
 and in front of them
     moe_rms_norm(x, weight, residual=None) -> y, or (y, x + residual)   (differentiable)
     moe_rms_norm_quant(x, weight, residual=None, fmt=QFMT_E4M3) -> (codes, scales, y, sum)
@@ -69,6 +70,7 @@ EXPORTS = ("moe_workspace_size", "moe_permute", "moe_grouped_gemm1_swiglu", "moe
            "moe_grouped_mm", "moe_grouped_mm_dgrad", "moe_grouped_mm_wgrad",
            "moe_grouped_mm_wgrad_workspace_size", "moe_quant_i8", "moe_mm_i8",
            "moe_linear_i8", "moe_linear_i8_workspace_size",
+           "moe_quant_mx4", "moe_mm_mx4", "moe_linear_mx4", "moe_linear_mx4_workspace_size",
            "moe_rms_norm", "moe_rms_norm_quant", "moe_rms_norm_backward", "moe_rms_norm_backward_workspace_size")
 
 # element types of the row-major products
@@ -138,6 +140,10 @@ def load(path: str = LIB_PATH) -> C.CDLL:
     L.moe_mm_i8.argtypes = [mmp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.moe_linear_i8_workspace_size.argtypes = [mmp, C.c_int, C.POINTER(sz)]
     L.moe_linear_i8.argtypes = [mmp, vp, C.c_int, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_quant_mx4.argtypes = [C.c_int, C.c_int, C.c_int, C.c_int, vp, vp, vp, vp]
+    L.moe_mm_mx4.argtypes = [mmp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.moe_linear_mx4_workspace_size.argtypes = [mmp, C.c_int, C.POINTER(sz)]
+    L.moe_linear_mx4.argtypes = [mmp, vp, C.c_int, vp, vp, vp, vp, vp, vp, sz, vp]
     normp = C.POINTER(MoeNormCfg)
     L.moe_rms_norm.argtypes = [normp, vp, vp, vp, vp, vp, vp, vp]
     L.moe_rms_norm_quant.argtypes = [normp, vp, vp, vp, vp, vp, vp, vp, vp]
@@ -766,6 +772,122 @@ def moe_linear_i8(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets: 
         work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     pk = None if work is None else _addr("work", work, (torch.uint8,), work.shape, dev)
     _call("moe_linear_i8", dev.index, C.byref(c), px, int(bool(swiglu)), pw, pws, po, pt, py, pk,
+          0 if work is None else work.numel())
+    if given is not None:
+        _written(given)
+    return out
+
+
+# ------------------------------------------------------------------ row-major MXFP4
+def moe_quant_mx4(x: torch.Tensor, swiglu: bool = False, codes: Optional[torch.Tensor] = None,
+                  scales: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """MXFP4 codes uint8 [R, K / 2] (two e2m1 per byte, the even column in the low
+    half) and e8m0 scales uint8 [R, K / 32] of the rows of x [R, K] (bfloat16 or
+    float16; activations or weights), or of silu(gate) * up with x [R, 2 K] =
+    gate | up where `swiglu`.  A block with an infinity or NaN gets the scale 255,
+    e8m0's NaN.  Not differentiable: operands that need a gradient are refused."""
+    _refuse_derivatives("moe_quant_mx4", None, x)
+    (R, width), dev = _rows_of("x", x), x.device
+    if swiglu and width % 2:
+        raise ValueError(f"x: {width} columns do not split into gate and up")
+    K = width // 2 if swiglu else width
+    px = _addr("x", x, _16BIT, (R, width), dev)
+    given = codes, scales
+    if codes is None:
+        codes = torch.empty(R, K // 2, dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty(R, K // 32, dtype=torch.uint8, device=dev)
+    pq = _addr("codes", codes, (torch.uint8,), (R, K // 2), dev)
+    ps = _addr("scales", scales, (torch.uint8,), (R, K // 32), dev)
+    _call("moe_quant_mx4", dev.index, R, K, _DT[x.dtype], int(bool(swiglu)), px, pq, ps)
+    for t in given:
+        if t is not None:
+            _written(t)
+    return codes, scales
+
+
+def _mx4_weights(wq, ws, offsets, dev):
+    """E, N, K and the addresses of MXFP4 weights [E, N, K / 2], or [N, K / 2] (dense:
+    no offsets), of their scales and of the offsets."""
+    if wq.dim() != (2 if offsets is None else 3):
+        raise ValueError(f"wq: [N, K / 2] without offsets, [E, N, K / 2] with offsets; got {tuple(wq.shape)}")
+    E, N, half = (1, *wq.shape) if offsets is None else wq.shape
+    if max(wq.shape) > 0x3FFFFFFF:
+        raise ValueError(f"wq: shape {tuple(wq.shape)}, sizes are at most 2^30 - 1")
+    pw = _addr("wq", wq, (torch.uint8,), wq.shape, dev)
+    ps = _addr("ws", ws, (torch.uint8,), (*wq.shape[:-1], half // 16), dev)
+    po = None if offsets is None else _addr("offsets", offsets, (torch.int32,), (E + 1,), dev)
+    return E, N, 2 * half, pw, ps, po
+
+
+def moe_mm_mx4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
+               offsets: Optional[torch.Tensor] = None, row_token: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """y[r] = x[t] @ w[e]^T with both operands in MXFP4 (moe_quant_mx4's codes and
+    scales), fp32 sums.
+
+    Dense: wq [N, K / 2], ws [N, K / 32], every row of xq.  Grouped: wq [E, N, K / 2],
+    ws [E, N, K / 32] and offsets int32 [E + 1]; with row_token int32 [R]
+    (moe_permute's) row r of the result takes row t = row_token[r] of xq, else t = r.
+    The result [R, N] is bfloat16 (default), float16 or float32; rows of no
+    group are zeros in a new result and stay as they are in a caller's `out`.
+    Not differentiable: outputs that need a gradient are refused."""
+    _refuse_derivatives("moe_mm_mx4", out)
+    (T, width), dev = _rows_of("xq", xq), xq.device
+    E, N, K, pw, pws, po = _mx4_weights(wq, ws, offsets, dev)
+    pq = _addr("xq", xq, (torch.uint8,), (T, K // 2), dev)
+    ps = _addr("xs", xs, (torch.uint8,), (T, K // 32), dev)
+    R, pt = _row_token(row_token, T, dev)
+    if out is not None and out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
+    given = out
+    out, clear = _new_or_checked(out, (R, N), out_dtype or torch.bfloat16, tuple(_DT), xq)
+    py = _addr("out", out, tuple(_DT), (R, N), dev)
+    c = MoeMmCfg(R, N, K, E, T, 0, _DT[out.dtype], clear)
+    _call("moe_mm_mx4", dev.index, C.byref(c), pq, ps, pw, pws, po, pt, py)
+    if given is not None:
+        _written(given)
+    return out
+
+
+def _linear_mx4_bytes(c: MoeMmCfg, gathered: int) -> int:
+    n = C.c_size_t(0)
+    _check("moe_linear_mx4_workspace_size",
+           (_lib or load()).moe_linear_mx4_workspace_size(C.byref(c), gathered, C.byref(n)))
+    return n.value
+
+
+def moe_linear_mx4_workspace_size(rows: int, K: int, out_rows: Optional[int] = None) -> int:
+    """Bytes of scratch moe_linear_mx4 needs for x of `rows` rows, K inputs of w
+    and, with row_token, `out_rows` rows of the result."""
+    return _linear_mx4_bytes(MoeMmCfg(rows if out_rows is None else out_rows, 8, K, 1, rows, 0, 0, 0),
+                             int(out_rows is not None))
+
+
+def moe_linear_mx4(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets: Optional[torch.Tensor] = None,
+                   row_token: Optional[torch.Tensor] = None, swiglu: bool = False, out: Optional[torch.Tensor] = None,
+                   out_dtype: Optional[torch.dtype] = None, work: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_mm_mx4 of moe_quant_mx4(x, swiglu): 16-bit activations (bfloat16 or
+    float16) times MXFP4 weights.  The result has x's type unless out_dtype or
+    `out` says otherwise.  `work`: uint8 scratch of at least
+    moe_linear_mx4_workspace_size(...) bytes, allocated where absent and needed.
+    Not differentiable: operands that need a gradient are refused."""
+    _refuse_derivatives("moe_linear_mx4", out, x)
+    (T, _), dev = _rows_of("x", x), x.device
+    E, N, K, pw, pws, po = _mx4_weights(wq, ws, offsets, dev)
+    px = _addr("x", x, _16BIT, (T, 2 * K if swiglu else K), dev)
+    R, pt = _row_token(row_token, T, dev)
+    if out is not None and out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out has dtype {out.dtype}, not {out_dtype}")
+    given = out
+    out, clear = _new_or_checked(out, (R, N), out_dtype or x.dtype, tuple(_DT), x)
+    py = _addr("out", out, tuple(_DT), (R, N), dev)
+    c = MoeMmCfg(R, N, K, E, T, _DT[x.dtype], _DT[out.dtype], clear)
+    if work is None:
+        need = _linear_mx4_bytes(c, int(row_token is not None))
+        work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    pk = None if work is None else _addr("work", work, (torch.uint8,), work.shape, dev)
+    _call("moe_linear_mx4", dev.index, C.byref(c), px, int(bool(swiglu)), pw, pws, po, pt, py, pk,
           0 if work is None else work.numel())
     if given is not None:
         _written(given)

@@ -421,6 +421,44 @@ int moe_linear_i8(const moe_mm_cfg* cfg, const void* x, int swiglu, const int8_t
                   void* stream);
 
 /* ------------------------------------------------------------------------
+ * MXFP4 on ROW-MAJOR operands (the layer's 4-bit format outside the layer:
+ * dense projections, shared experts, experts that are not prepacked): e2m1
+ * codes packed two per byte (even K index in the low nibble) with one e8m0
+ * scale per 32 along K, as in the canonical MXFP4 weights above.
+ *
+ * Quantisation of 16-bit rows (activations, or weights when they are loaded):
+ * per 32 consecutive values with the greatest magnitude a, X =
+ * 2^(floor(log2 a) - 2) clamped to the e8m0 range (a = 0: 2^-127), code =
+ * e2m1(v / X) rounded to nearest even, saturating at +-6: the layer's 4-bit
+ * activation rule.  A block that holds an infinity or NaN gets codes 0 and the
+ * scale 255 (NaN), so that every result made from it is NaN.
+ *   x      [R][K] of dtype; swiglu = 1: [R][2 K], v = silu(x[:, :K]) *
+ *          x[:, K:] in fp32
+ *   codes  uint8 [R][K / 2]; scales uint8 [R][K / 32]
+ * K a multiple of 32 up to 2^20 (MOE_ERR_BAD_SHAPE otherwise). */
+int moe_quant_mx4(int R, int K, int dtype, int swiglu, const void* x, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* The product y[r][n] = sum_k xq_deq[t][k] * wq_deq[e][n][k], t =
+ * row_token[r], or r where row_token is NULL; fp32 sums, one rounding.
+ *   xq uint8 [T][K / 2] and xs uint8 [T][K / 32] with row_token, else R rows
+ *   wq uint8 [E][N][K / 2]; ws uint8 [E][N][K / 32]
+ *   offsets, row_token, y: as in moe_mm_i8 (offsets NULL: one dense matrix); a
+ *   row whose index lies outside [0, T) counts as a row of zeros
+ * N a multiple of 8, K of 32, both up to 2^20; with row_token T * K < 2^32
+ * (MOE_ERR_BAD_SHAPE otherwise).  cfg->dtype is not used. */
+int moe_mm_mx4(const moe_mm_cfg* cfg, const uint8_t* xq, const uint8_t* xs, const uint8_t* wq, const uint8_t* ws,
+               const int32_t* offsets, const int32_t* row_token, void* y, void* stream);
+
+/* moe_quant_mx4 of x and moe_mm_mx4 in one call.
+ *   x  of dtype, [T][K] with row_token, else [R][K] (swiglu = 1: 2 K wide)
+ *   work: device scratch of moe_linear_mx4_workspace_size(cfg, row_token !=
+ *   NULL) bytes (contents on entry ignored; NULL when that size is 0). */
+int moe_linear_mx4_workspace_size(const moe_mm_cfg* cfg, int gathered, size_t* bytes);
+int moe_linear_mx4(const moe_mm_cfg* cfg, const void* x, int swiglu, const uint8_t* wq, const uint8_t* ws,
+                   const int32_t* offsets, const int32_t* row_token, void* y, void* work, size_t work_bytes,
+                   void* stream);
+
+/* ------------------------------------------------------------------------
  * Root-mean-square norm with the residual's addition, in front of the router
  * and of the products: for each row
  *   s = x + residual, rounded to the rows' type (without residual s = x),
