@@ -25,6 +25,7 @@ and on row-major weights (nothing to prepack):
     moe_mm_i8(xq, xs, wq, ws, offsets=None, row_token=None) -> y   (grouped or dense)
     moe_linear_i8(x, wq, ws, offsets=None, row_token=None, swiglu=False) -> y   (both in one call)
     moe_quant_mx4, moe_mm_mx4, moe_linear_mx4   (the same three in MXFP4: e2m1 codes, an e8m0 scale per 32)
+    moe_layer_mm(x, topk_ids, topk_weights, w1, w2) -> out   (the whole layer for up to 64 tokens, 16-bit experts)
 and in front of them
     moe_rms_norm(x, weight, residual=None) -> y, or (y, x + residual)   (differentiable)
     moe_rms_norm_quant(x, weight, residual=None, fmt=QFMT_E4M3) -> (codes, scales, y, sum)
@@ -71,6 +72,7 @@ EXPORTS = ("moe_workspace_size", "moe_permute", "moe_grouped_gemm1_swiglu", "moe
            "moe_grouped_mm_wgrad_workspace_size", "moe_quant_i8", "moe_mm_i8",
            "moe_linear_i8", "moe_linear_i8_workspace_size",
            "moe_quant_mx4", "moe_mm_mx4", "moe_linear_mx4", "moe_linear_mx4_workspace_size",
+           "moe_layer_mm", "moe_layer_mm_workspace_size",
            "moe_rms_norm", "moe_rms_norm_quant", "moe_rms_norm_backward", "moe_rms_norm_backward_workspace_size")
 
 # element types of the row-major products
@@ -89,6 +91,10 @@ class MoeWeights(C.Structure):
 
 class MoeMmCfg(C.Structure):
     _fields_ = [(n, C.c_int32) for n in ("R", "N", "K", "E", "T", "dtype", "out_dtype", "clear_rest")]
+
+
+class MoeFewCfg(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("T", "H", "I", "E", "topk", "dtype")]
 
 
 class MoeNormCfg(C.Structure):
@@ -144,6 +150,9 @@ def load(path: str = LIB_PATH) -> C.CDLL:
     L.moe_mm_mx4.argtypes = [mmp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.moe_linear_mx4_workspace_size.argtypes = [mmp, C.c_int, C.POINTER(sz)]
     L.moe_linear_mx4.argtypes = [mmp, vp, C.c_int, vp, vp, vp, vp, vp, vp, sz, vp]
+    fewp = C.POINTER(MoeFewCfg)
+    L.moe_layer_mm.argtypes = [fewp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_layer_mm_workspace_size.argtypes = [fewp, C.POINTER(sz)]
     normp = C.POINTER(MoeNormCfg)
     L.moe_rms_norm.argtypes = [normp, vp, vp, vp, vp, vp, vp, vp]
     L.moe_rms_norm_quant.argtypes = [normp, vp, vp, vp, vp, vp, vp, vp, vp]
@@ -889,6 +898,60 @@ def moe_linear_mx4(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets:
     pk = None if work is None else _addr("work", work, (torch.uint8,), work.shape, dev)
     _call("moe_linear_mx4", dev.index, C.byref(c), px, int(bool(swiglu)), pw, pws, po, pt, py, pk,
           0 if work is None else work.numel())
+    if given is not None:
+        _written(given)
+    return out
+
+
+# ------------------------------------------------------------------ the layer for a few tokens
+def _few_bytes(c: MoeFewCfg) -> int:
+    n = C.c_size_t(0)
+    _check("moe_layer_mm_workspace_size", (_lib or load()).moe_layer_mm_workspace_size(C.byref(c), C.byref(n)))
+    return n.value
+
+
+def moe_layer_mm_workspace_size(T: int, H: int, I: int, E: int, topk: int) -> int:
+    """Bytes of scratch moe_layer_mm needs for T tokens."""
+    return _few_bytes(MoeFewCfg(T, H, I, E, topk, 0))
+
+
+def moe_layer_mm(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor, w1: torch.Tensor,
+                 w2: torch.Tensor, out: Optional[torch.Tensor] = None,
+                 ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out [T, H] = sum over j of topk_weights[t, j] * w2[e] (silu(g) * u) with (g, u) =
+    w1[e] x[t] and e = topk_ids[t, j], for up to 64 tokens: the whole expert layer on
+    16-bit row-major weights in two launches.
+
+    x [T, H], w1 [E, 2 I, H] (gate rows first) and w2 [E, H, I] are all bfloat16 or all
+    float16; topk_ids int32 and topk_weights float32 [T, topk] as moe_route gives
+    them.  Ids outside [0, E) are masked slots.  `ws`: uint8 scratch of at least
+    moe_layer_mm_workspace_size(...) bytes, allocated where absent; calls that share
+    one must not overlap.  An always-on shared expert is one more matrix pair behind
+    the others, named by one more slot of weight 1.  For more tokens use moe_grouped_mm
+    (MOE_ERR_UNSUPPORTED here).  Not differentiable: operands that need a gradient are refused."""
+    _refuse_derivatives("moe_layer_mm", out, x, topk_weights)
+    _refuse_derivatives("moe_layer_mm", None, w1, w2)
+    (T, H), dt, dev = _rows_of("x", x), x.dtype, x.device
+    topk = _rows_of("topk_ids", topk_ids)[1]
+    E, two, _ = _matrices(w1)
+    if two % 2:
+        raise ValueError(f"w1: {two} rows do not split into gate and up")
+    I = two // 2
+    px = _addr("x", x, _16BIT, (T, H), dev)
+    pi = _addr("topk_ids", topk_ids, (torch.int32,), (T, topk), dev)
+    pt = _addr("topk_weights", topk_weights, (torch.float32,), (T, topk), dev)
+    p1 = _addr("w1", w1, (dt,), (E, two, H), dev)
+    p2 = _addr("w2", w2, (dt,), (E, H, I), dev)
+    given = out
+    if out is None:
+        out = torch.empty_like(x)
+    po = _addr("out", out, (dt,), (T, H), dev)
+    c = MoeFewCfg(T, H, I, E, topk, _DT[dt])
+    if ws is None:
+        need = _few_bytes(c)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    pk = None if ws is None else _addr("ws", ws, (torch.uint8,), ws.shape, dev)
+    _call("moe_layer_mm", dev.index, C.byref(c), px, pi, pt, p1, p2, po, pk, 0 if ws is None else ws.numel())
     if given is not None:
         _written(given)
     return out

@@ -459,6 +459,36 @@ int moe_linear_mx4(const moe_mm_cfg* cfg, const void* x, int swiglu, const uint8
                    void* stream);
 
 /* ------------------------------------------------------------------------
+ * The whole expert layer for a FEW tokens on 16-bit ROW-MAJOR weights (experts
+ * that are not quantised), in two launches and without a permuted copy of the
+ * tokens:
+ *   out[t] = sum over j of topk_weights[t][j] * W2[e] (silu(g) * u),
+ *   (g, u) = W1[e] x[t],  e = topk_ids[t][j]
+ * fp32 sums, out rounded once.  Between the products h = silu(g) * u is kept as
+ * the sum of two values of dtype (past fp16's range it is infinite).  The weights
+ * of an expert that some token names are read once, the others not at all.
+ *
+ * moe_few_cfg (host struct): T tokens (0 .. 64), H hidden size and I expert
+ *   width (multiples of 8 up to 2^16), E experts (up to 1024), topk slots per
+ *   token (up to 32), dtype of x, w1, w2 and out (MOE_DT_BF16 / MOE_DT_FP16).
+ *   More tokens are MOE_ERR_UNSUPPORTED: there moe_grouped_mm is the one to use.
+ *   x [T][H]; topk_ids int32 [T][topk]: ids outside [0, E) are masked slots (no
+ *   contribution), the same expert may come twice; topk_weights fp32 [T][topk]
+ *   w1 [E][2 I][H], gate rows first; w2 [E][H][I]
+ *   out [T][H]; overlaps no operand
+ *   ws: device scratch of moe_layer_mm_workspace_size(cfg) bytes (contents on
+ *   entry ignored; NULL for T = 0).  Calls that share one must not overlap.
+ * topk_ids and topk_weights need 4-byte alignment only.  Equal inputs give equal
+ * bits, but for a token that names an expert twice. */
+typedef struct moe_few_cfg {
+  int32_t T, H, I, E, topk;
+  int32_t dtype;
+} moe_few_cfg;
+int moe_layer_mm_workspace_size(const moe_few_cfg* cfg, size_t* bytes);
+int moe_layer_mm(const moe_few_cfg* cfg, const void* x, const int32_t* topk_ids, const float* topk_weights,
+                 const void* w1, const void* w2, void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Root-mean-square norm with the residual's addition, in front of the router
  * and of the products: for each row
  *   s = x + residual, rounded to the rows' type (without residual s = x),
