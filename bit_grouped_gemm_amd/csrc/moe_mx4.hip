@@ -350,32 +350,34 @@ __global__ __launch_bounds__(kThreads, 1) void k_mx4(Mx4Args a) {
   const long wrow = long(pl.e) * a.N + n0;
   qs.init(static_cast<const uint8_t*>(a.q) + wrow * ld, grouped ? long(min(kBN, a.N - n0)) * ld : 0, ld, w, lane,
           nullptr, 0, 0);
-  // scales: a thread has one column's row and one of the rows
-  const uint8_t *qe = nullptr, *pe = nullptr;
-  if (grouped) {
-    const int r = threadIdx.x;
-    if (n0 + r < a.N) qe = a.qe + (wrow + r) * nb;
-    if (r < pl.rows) {
-      const int t = token_of(a, pl.row0 + r);
-      if (t >= 0) pe = a.pe + long(t) * nb;
+  // scales: two lanes have a row's 32 bytes, lane l half l % 2 of row l / 2 of a wave's 32
+  constexpr int kSets = (kBN + BM) / 128;
+  const uint8_t* se[kSets];
+#pragma unroll
+  for (int i = 0; i < kSets; ++i) {
+    const int r = i * 128 + w * 32 + (lane >> 1), part = (lane & 1) * 16;
+    se[i] = nullptr;
+    if (!grouped) continue;
+    if (i < 2) {
+      if (n0 + r < a.N) se[i] = a.qe + (wrow + r) * nb + part;
+    } else if (r - kBN < pl.rows) {
+      const int t = token_of(a, pl.row0 + r - kBN);
+      if (t >= 0) se[i] = a.pe + long(t) * nb + part;
     }
   }
-  v4i next[4];
+  v4i next[kSets];
   auto fetch = [&](int s) __attribute__((always_inline)) {  // of steps s .. s + 3
-    const int at = s * 8, left = nb - at;
-    next[0] = load_scales16(qe + at, qe ? left : 0);
-    next[1] = load_scales16(qe + at + 16, qe ? left - 16 : 0);
-    next[2] = load_scales16(pe + at, pe ? left : 0);
-    next[3] = load_scales16(pe + at + 16, pe ? left - 16 : 0);
+    const int at = s * 8, left = nb - at - (lane & 1) * 16;
+#pragma unroll
+    for (int i = 0; i < kSets; ++i) next[i] = load_scales16(se[i] + at, se[i] ? left : 0);
   };
   auto put = [&](uint8_t* s) __attribute__((always_inline)) {
-    const int r = threadIdx.x, x = (r >> 3 & 3) * 8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i >= 2 && r >= BM) break;
-      uint8_t* to = s + ((i >> 1) * kBN + r) * 32;
-      *reinterpret_cast<int2*>(to + (((i & 1) * 16) ^ x)) = make_int2(next[i][0], next[i][1]);
-      *reinterpret_cast<int2*>(to + (((i & 1) * 16 + 8) ^ x)) = make_int2(next[i][2], next[i][3]);
+    for (int i = 0; i < kSets; ++i) {
+      const int r = i * 128 + w * 32 + (lane >> 1), part = (lane & 1) * 16, x = (r >> 3 & 3) * 8;
+      uint8_t* to = s + r * 32;
+      *reinterpret_cast<int2*>(to + (part ^ x)) = make_int2(next[i][0], next[i][1]);
+      *reinterpret_cast<int2*>(to + ((part + 8) ^ x)) = make_int2(next[i][2], next[i][3]);
     }
   };
 
