@@ -86,6 +86,22 @@ __device__ __forceinline__ int2 group_rows(const int32_t* offsets, int e, int E,
   return make_int2(a, b);
 }
 
+// The sums of the lanes up to each one, saturating: within 16 lanes, then the rows of 16
+// before it (lane moves inside the vector unit: each is some ten cycles, a shuffle through
+// LDS a hundred).
+__device__ __forceinline__ int wave_scan_sat(int v) {
+#define MOE_SCAN(CTRL, ROWS) \
+  v = __builtin_elementwise_add_sat(v, __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false))
+  MOE_SCAN(0x111, 0xF);  // row_shr:1
+  MOE_SCAN(0x112, 0xF);
+  MOE_SCAN(0x114, 0xF);
+  MOE_SCAN(0x118, 0xF);
+  MOE_SCAN(0x142, 0xA);  // row_bcast:15 into rows 1 and 3
+  MOE_SCAN(0x143, 0xC);  // row_bcast:31 into rows 2 and 3
+#undef MOE_SCAN
+  return v;
+}
+
 // Tile `t` of the launch: every wave scans the groups' tile counts (64 lanes
 // at a time), so nothing has to be prepared on the host.  `id` runs over this
 // launch's workgroups; workgroup ids are dealt round-robin over the 8 XCDs,
@@ -107,12 +123,7 @@ __device__ __forceinline__ bool find_tile(const MmArgs& a, int BM, int ncol, int
       r = group_rows(a.offsets, e0 + lane, a.E, a.R);
       n = (r.y - r.x + BM - 1) / BM;
     }
-    incl = n;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(incl, d, 64);
-      if (lane >= d) incl = __builtin_elementwise_add_sat(incl, v);
-    }
+    incl = wave_scan_sat(n);
   };
   int total = 0;
   for (int e0 = 0; e0 < G; e0 += 64) {

@@ -342,14 +342,17 @@ __global__ __launch_bounds__(kThreads, 1) void k_mx4(Mx4Args a) {
   ct = __builtin_amdgcn_readfirstlane(ct);
   const bool grouped = pl.e < a.E;
   const int n0 = ct * kBN, steps = grouped ? (ld + 127) / 128 : 0;
-  PS ps;
-  QS qs;
-  const uint8_t* P = static_cast<const uint8_t*>(a.p);
-  if (a.row_token) ps.init(P, long(a.T) * ld, ld, w, lane, a.row_token + pl.row0, pl.rows, a.T);
-  else ps.init(P + long(pl.row0) * ld, long(pl.rows) * ld, ld, w, lane, nullptr, 0, 0);
   const long wrow = long(pl.e) * a.N + n0;
+  // The first loads go out as early as they can: the columns', then, with the rows'
+  // places known, the rows'.
+  QS qs;
   qs.init(static_cast<const uint8_t*>(a.q) + wrow * ld, grouped ? long(min(kBN, a.N - n0)) * ld : 0, ld, w, lane,
           nullptr, 0, 0);
+  qs.issue(q0, w, ld);
+  PS ps;
+  const uint8_t* P = static_cast<const uint8_t*>(a.p);
+  if (a.row_token) ps.init(P, grouped ? long(a.T) * ld : 0, ld, w, lane, a.row_token + pl.row0, pl.rows, a.T);
+  else ps.init(P + long(pl.row0) * ld, grouped ? long(pl.rows) * ld : 0, ld, w, lane, nullptr, 0, 0);
   // scales: two lanes have a row's 32 bytes, lane l half l % 2 of row l / 2 of a wave's 32
   constexpr int kSets = (kBN + BM) / 128;
   const uint8_t* se[kSets];
@@ -365,6 +368,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_mx4(Mx4Args a) {
       if (t >= 0) se[i] = a.pe + long(t) * nb + part;
     }
   }
+  ps.issue(p0, w, ld);
   v4i next[kSets];
   auto fetch = [&](int s) __attribute__((always_inline)) {  // of steps s .. s + 3
     const int at = s * 8, left = nb - at - (lane & 1) * 16;
@@ -389,7 +393,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_mx4(Mx4Args a) {
 #pragma unroll
       for (int u = 0; u < 16; ++u) acc[i][j][u] = 0.0f;
 
-  int kleft = ld;  // bytes of a row from the next step to load on
+  int kleft = ld - 128;  // bytes of a row from the next step to load on
   auto issue = [&](uint8_t* sp, uint8_t* sq) __attribute__((always_inline)) {
     ps.issue(sp, w, kleft);
     qs.issue(sq, w, kleft);
@@ -481,9 +485,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_mx4(Mx4Args a) {
   auto scales_of = [&](int s) __attribute__((always_inline)) { return sc + (s / kGroupSteps & 1) * kGroup; };
   if (steps) {
     fetch(0);
-    issue(p0, q0);
-    put(sc);
     issue(p1, q1);
+    put(sc);
     stage_barrier_but<PS::kLoads + QS::kLoads>();
     read(f0, p0, q0, 0);
     read_scales(now, sc, 0);
@@ -584,6 +587,24 @@ bool plan(const Mx4Args& a, TileShape* s, long* grid) {
   return *grid <= max_blocks(kThreads);
 }
 
+// Rows of a dense product's first launch.  Where the last few rows would make the
+// large tiles go one more round, they go into a launch of their own, in the shape
+// that suits them; a launch counts as much as bringing in kLaunchBytes.
+constexpr double kLaunchBytes = 250e3;
+int first_rows(const Mx4Args& a) {
+  if (a.offsets || a.R <= 256) return a.R;
+  const int rows = a.R / 256 * 256;
+  if (rows == a.R) return a.R;
+  double one, head, tail;
+  shape_of(a, &one);
+  Mx4Args h = a, t = a;
+  h.R = rows;
+  t.R = a.R - rows;
+  shape_of(h, &head);
+  shape_of(t, &tail);
+  return head + tail + kLaunchBytes / (a.K / 2) < one ? rows : a.R;
+}
+
 hipError_t launch_one(const Mx4Args& a, const TileShape& s, long grid, hipStream_t st) {
   static_assert(kThreads == kFewWaves * 64, "one limit of a launch");
   if (grid == 0) return hipSuccess;
@@ -615,10 +636,26 @@ bool mx4_too_large(const Mx4Args& a) {
 }
 
 hipError_t launch_mx4(const Mx4Args& a, hipStream_t st, bool* too_large) {
-  TileShape s;
-  long grid;
+  TileShape s, ts;
+  long grid, tail_grid;
   *too_large = !plan(a, &s, &grid);
-  return *too_large ? hipSuccess : launch_one(a, s, grid, st);
+  if (*too_large) return hipSuccess;
+  const int rows = first_rows(a);
+  if (rows == a.R) return launch_one(a, s, grid, st);
+  Mx4Args head = a, tail = a;
+  head.R = rows;
+  tail.R = a.R - rows;
+  tail.out = static_cast<uint8_t*>(a.out) + long(rows) * a.N * (a.out_ty == kFp32 ? 4 : 2);
+  if (a.row_token) {
+    tail.row_token = a.row_token + rows;
+  } else {
+    tail.p = static_cast<const uint8_t*>(a.p) + long(rows) * (a.K / 2);
+    tail.pe = a.pe + long(rows) * (a.K / 32);
+  }
+  *too_large = !plan(head, &s, &grid) || !plan(tail, &ts, &tail_grid);
+  if (*too_large) return hipSuccess;
+  const hipError_t e = launch_one(head, s, grid, st);
+  return e != hipSuccess ? e : launch_one(tail, ts, tail_grid, st);
 }
 
 template <int TY, bool GLU>
