@@ -264,6 +264,251 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_mx4_few(Mx4Args a) {
   }
 }
 
+// Many small groups (a decode batch's experts): 16 rows by 64 columns per wave, all of K,
+// nothing shared between the four waves of a workgroup but their rows.  Lanes load
+// matrix fragments straight into registers, D steps ahead, so there is no stage to
+// fill and no sum to join.  Bound by the weights' bytes: 61 tokens, top-8 of 64, 2048 ->
+// 7168: 106 us, 4.7 TB/s of weights, where k_mx4_few takes 147.
+constexpr int kDirectCols = 64;  // of a wave
+
+template <int D>
+__global__ __launch_bounds__(256) void k_mx4_direct(Mx4Args a) {
+  constexpr int NC = kDirectCols / 16;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = lane & 15, g = lane >> 4;
+  const int ncol = (a.N + 4 * kDirectCols - 1) / (4 * kDirectCols);
+  Place pl;
+  int ct;
+  if (!find_tile(a, 16, ncol, blockIdx.x, pl, ct)) return;
+  const int n0 = (ct * 4 + w) * kDirectCols, ld = a.K / 2, nb = a.K / 32;
+  if (n0 >= a.N) return;
+  const bool grouped = pl.e < a.E;
+  const int t = m < pl.rows ? token_of(a, pl.row0 + m) : 0;
+  v4f acc[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  if (grouped) {
+    // Lane l has row l % 16 of each fragment, bytes 64 h + 16 (l / 16) + 0..15 of half h of a step.
+    // Columns and rows behind the last, and rows that name no token, take the values of
+    // one that is there: their results are not stored, or stored as zeros.
+    const uint8_t *pw[NC], *qe[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const long row = long(pl.e) * a.N + min(n0 + i * 16 + m, a.N - 1);
+      pw[i] = static_cast<const uint8_t*>(a.q) + row * ld + 16 * g;
+      qe[i] = a.qe + row * nb;
+    }
+    const bool none = a.row_token && a.T == 0;
+    const long row = none ? 0 : a.row_token ? max(t, 0) : pl.row0 + (m < pl.rows ? m : 0);
+    const uint8_t* pp = static_cast<const uint8_t*>(none ? a.q : a.p) + row * ld + 16 * g;
+    const uint8_t* pe = (none ? a.qe : a.pe) + row * nb;
+    struct Step {
+      v4i w[NC][2], p[2];
+      uint2 qe[NC], pe;  // the eight scales of the row's step
+    };
+    auto load = [&](Step& s, int at) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s.w[i][h] = *reinterpret_cast<const v4i*>(pw[i] + at * 128 + 64 * h);
+        __builtin_memcpy(&s.qe[i], qe[i] + at * 8, 8);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) s.p[h] = *reinterpret_cast<const v4i*>(pp + at * 128 + 64 * h);
+      __builtin_memcpy(&s.pe, pe + at * 8, 8);
+    };
+    auto use = [&](const Step& s) __attribute__((always_inline)) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+          acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              operand(s.w[i][h]), operand(s.p[h]), acc[i], kFmtE2M1, kFmtE2M1, 0, (h ? s.qe[i].y : s.qe[i].x) >> (8 * g), 0,
+              (h ? s.pe.y : s.pe.x) >> (8 * g));
+    };
+    const int n = ld / 128;  // whole steps
+    Step s[D];
+    if (n > 0) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) load(s[d], min(d, n - 1));
+      int k = 0;
+      for (; k + D <= n; k += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          use(s[d]);
+          load(s[d], min(k + d + D, n - 1));  // (the last ones again where there are no more)
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+        if (k + d < n) use(s[d]);
+    }
+    const int left = nb - n * 8;  // the rest of K: 1 to 7 blocks, zeros behind them
+    if (left) {
+      auto rest = [&](const uint8_t* p, int h) __attribute__((always_inline)) {
+        return 4 * h + g < left ? *reinterpret_cast<const v4i*>(p + n * 128 + 64 * h) : v4i{0, 0, 0, 0};
+      };
+      auto rest_scales = [&](const uint8_t* p) __attribute__((always_inline)) {
+        uint2 v = make_uint2(0, 0);  // this lane's two, where the shift of `use` finds them
+        if (g < left) v.x = uint32_t(p[n * 8 + g]) << (8 * g);
+        if (4 + g < left) v.y = uint32_t(p[n * 8 + 4 + g]) << (8 * g);
+        return v;
+      };
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        s[0].w[i][0] = rest(pw[i], 0);
+        s[0].w[i][1] = rest(pw[i], 1);
+        s[0].qe[i] = rest_scales(qe[i]);
+      }
+      s[0].p[0] = rest(pp, 0);
+      s[0].p[1] = rest(pp, 1);
+      s[0].pe = rest_scales(pe);
+      use(s[0]);
+    }
+  }
+  // lane l holds columns 4 (l / 16) + 0..3 of row l % 16 of each fragment
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = n0 + i * 16 + 4 * g;
+    if (m < pl.rows && c < a.N)
+      store4(a.out, (long(pl.row0) + m) * a.N + c, t < 0 ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : acc[i], a.out_ty);
+  }
+}
+
+// moe_linear_mx4 for one row: k_mx4_few with the quantiser in front, in every
+// workgroup: its lanes quantise the row while the first weights are on their
+// way; codes and scales stay in LDS, where all K steps read them.  Codes, sums and
+// results are those of the two launches it stands for.
+constexpr int kOneChunks = 4;  // chunks of 8 values that a lane has
+constexpr int kOneMaxK = kOneChunks * kFewWaves * 64 * 8;
+
+template <int XT, bool GLU, int NC>
+__global__ __launch_bounds__(kFewWaves * 64) void k_mx4_one(Mx4Args a) {
+  constexpr int S = 4, L = 2 * NC, kStage = L * 1024;
+  __shared__ __align__(1024) uint8_t st0[kFewWaves * kStage];
+  __shared__ __align__(1024) uint8_t st1[kFewWaves * kStage];
+  __shared__ __align__(1024) uint8_t st2[kFewWaves * kStage];
+  __shared__ __align__(1024) uint8_t st3[kFewWaves * kStage];
+  __shared__ __align__(1024) uint8_t scales[kFewWaves * 1024];
+  __shared__ __align__(16) uint8_t codes[kOneMaxK / 2];
+  __shared__ __align__(16) uint8_t xscales[kOneMaxK / 32];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = lane & 15, g = lane >> 4;
+  const int ncol = (a.N + 16 * NC - 1) / (16 * NC);
+  Place pl;
+  int ct;
+  if (!find_tile(a, 16, ncol, blockIdx.x, pl, ct)) return;
+  const int K = a.K, ld = K / 2, nb = K / 32, n0 = ct * 16 * NC;
+  const bool grouped = pl.e < a.E;  // else the row belongs to no group: zeros
+  const int steps = grouped ? (ld + 127) / 128 : 0;
+  const int each = (steps + kFewWaves - 1) / kFewWaves;
+  const int s0 = w * each, mine = max(0, min(steps - s0, each));
+  const long wrow = long(grouped ? pl.e : 0) * a.N + n0;
+  const uint8_t* wq = static_cast<const uint8_t*>(a.q) + wrow * ld;
+  const int wrows = min(16 * NC, a.N - n0);
+  const uint32_t wspan = uint32_t(wrows) * uint32_t(ld);
+  const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+  uint32_t ow[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) ow[i] = uint32_t(8 * i + (lane >> 3)) * uint32_t(ld) + chunk;
+  auto issue = [&](uint8_t* stage, int k) __attribute__((always_inline)) {
+    const int at = (s0 + k) * 128;
+    const bool in = k < mine && chunk < ld - at;
+#pragma unroll
+    for (int i = 0; i < L; ++i) dma16<true>(wq, wspan, in ? ow[i] + at : kOutside, stage + w * kStage + i * 1024);
+  };
+  // the weights' scales, four steps at a time: as in k_mx4_few
+  const uint8_t* se = (lane >> 1) < wrows && grouped ? a.qe + (wrow + (lane >> 1)) * nb + (lane & 1) * 16 : nullptr;
+  v4i next;
+  auto fetch = [&](int k) __attribute__((always_inline)) {
+    const int at = (s0 + k) * 8;
+    next = load_scales16(se + at, se && k < mine ? nb - at - (lane & 1) * 16 : 0);
+  };
+  uint8_t* mys = scales + w * 1024;
+
+  // the row comes in ahead of the first weights; one that names no token is zeros
+  const int t = grouped ? token_of(a, pl.row0) : -1;
+  const uint16_t* x = static_cast<const uint16_t*>(a.p) + long(max(t, 0)) * (GLU ? 2L * K : K);
+  quant_raw8 raw[kOneChunks][GLU ? 2 : 1];
+#pragma unroll
+  for (int i = 0; i < kOneChunks; ++i) {
+    const int c = (i * kFewWaves * 64 + int(threadIdx.x)) * 8;
+#pragma unroll
+    for (int h = 0; h < (GLU ? 2 : 1); ++h)
+      raw[i][h] = t >= 0 && c < K ? *reinterpret_cast<const quant_raw8*>(x + h * K + c) : quant_raw8{0, 0, 0, 0};
+  }
+  fetch(0);
+  __builtin_amdgcn_sched_barrier(0);
+  issue(st0, 0);
+  issue(st1, 1);
+  issue(st2, 2);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < kOneChunks; ++i) {
+    const int c = (i * kFewWaves * 64 + int(threadIdx.x)) * 8;
+    const f8v v = quant_value8<XT, GLU>(raw[i][0], raw[i][GLU ? 1 : 0]);
+    const uint32_t scale = mx4_scale(group_top_dpp(quant_top8(v), 4));
+    // the last step's columns past K are zeros
+    if (c < (K + 255) / 256 * 256) {
+      *reinterpret_cast<uint32_t*>(codes + c / 2) = mx4_codes8(v, scale);
+      if (c % 32 == 0) xscales[c / 32] = uint8_t(scale);
+    }
+  }
+  lds_barrier();
+
+  v4f acc[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  auto multiply = [&](const uint8_t* stage, int k) __attribute__((always_inline)) {
+    wait_vm<(S - 1) * L>();
+    __builtin_amdgcn_sched_barrier(0);
+    const bool has = m == 0 && k < mine;
+    const int pe = has ? *reinterpret_cast<const uint16_t*>(xscales + (s0 + k) * 8 + 2 * g) : 0;
+    int qe[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      qe[i] = *reinterpret_cast<const uint16_t*>(mys + (i * 16 + m) * 32 + (k & 3) * 8 + 2 * g);
+    auto half = [&](auto kk) __attribute__((always_inline)) {
+      v4i pf = {0, 0, 0, 0};
+      if (has) pf = *reinterpret_cast<const v4i*>(codes + (s0 + k) * 128 + (2 * g + kk) * 16);
+      const int slot = ((2 * g + kk) ^ (m & 7)) << 4;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const v4i qf = *reinterpret_cast<const v4i*>(stage + w * kStage + (i * 16 + m) * 128 + slot);
+        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(qf), operand(pf), acc[i], kFmtE2M1, kFmtE2M1, kk,
+                                                                qe[i], kk, pe);
+      }
+    };
+    half(std::integral_constant<int, 0>{});
+    half(std::integral_constant<int, 1>{});
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  for (int k = 0; k < mine; k += kGroupSteps) {
+    *reinterpret_cast<v4i*>(mys + lane * 16) = next;
+    fetch(k + kGroupSteps);
+    __builtin_amdgcn_sched_barrier(0);
+    issue(st3, k + 3); multiply(st0, k);
+    issue(st0, k + 4); multiply(st1, k + 1);
+    issue(st1, k + 5); multiply(st2, k + 2);
+    issue(st2, k + 6); multiply(st3, k + 3);
+  }
+  stage_barrier();  // every load has landed: the first stage takes the sums
+  v4f* part = reinterpret_cast<v4f*>(st0);
+#pragma unroll
+  for (int i = 0; i < NC; ++i) part[(w * NC + i) * 64 + lane] = acc[i];
+  __syncthreads();
+  if (w < NC && m == 0) {  // fragment w: lane l holds columns 4 (l / 16) + 0..3 of row l % 16
+    v4f sum = part[w * 64 + lane];
+#pragma unroll
+    for (int u = 1; u < kFewWaves; ++u) sum += part[(u * NC + w) * 64 + lane];
+    const int c = n0 + w * 16 + 4 * g;
+    if (c < a.N) store4(a.out, long(pl.row0) * a.N + c, t < 0 ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : sum, a.out_ty);
+  }
+}
+
 // Where there are tiles enough: 256 columns by BM rows per workgroup, four waves of
 // BM / 2 rows by 128 columns each, so that a wave reads every fragment for four
 // instructions and a SIMD's registers hold one wave's sums.  Two stages of a K
@@ -545,25 +790,39 @@ __global__ __launch_bounds__(kThreads, 1) void k_mx4(Mx4Args a) {
   else put_out(std::integral_constant<int, kBf16>{});
 }
 
+// The shape of a launch: rows and columns of a tile, and the kernel that makes it.
+enum { kBig, kFew, kDirect };
 struct TileShape {
-  int few, rows, cols;
+  int kind, rows, cols;
 };
 
-// The tile shape whose launch brings the fewest bytes through a CU: rounds of one
-// tile per CU times (rows + columns) of a tile.  The row tiles of ragged groups are
-// estimated: groups with a row, each half a tile more than its mean needs.  Among
-// equals the first.
+// The shape that is expected to take the least time, in us: rounds of one tile per CU,
+// each a fixed time plus the bytes of its rows and columns at a rate, both as measured per
+// kernel.  (Calls of one matrix, K = N = 4096, us: 64 rows in 32 x 32 tiles 14.1, 16 x 32 14.8,
+// 64 x 64 15.0; 600 rows in 128 x 256 21, 64 x 64 28, 256 x 256 29; 2048 rows 26, 70, 33.  Top-8
+// of 64: 61 tokens, 2048 -> 7168, direct 112, 128 x 256 113, 16 x 64 147; 512 -> 2048: 18, 19, 61;
+// 512 tokens, 4096 -> 1536: 128 x 256 58, 256 x 256 68, 64 x 64 93; 1024 tokens, 2048 -> 1408: 256
+// x 256 43, 128 x 256 45.  About 10 us of each are the call's.)
+// The row tiles of ragged groups are estimated: groups with a row, each half a tile more
+// than its mean needs.
 TileShape shape_of(const Mx4Args& a, double* cost_of = nullptr) {
-  static const TileShape shapes[] = {{1, 16, 64}, {1, 16, 32}, {1, 16, 16}, {1, 32, 32}, {1, 32, 64},
-                                     {1, 32, 16}, {1, 64, 64}, {1, 64, 32}, {1, 64, 16}, {0, 128, kBN}, {0, 256, kBN}};
+  struct Cost {
+    double fixed, rate;
+  };
+  static const Cost cost_of_kind[] = {{10, 40e3}, {4.5, 45e3}, {2, 21e3}};
+  static const TileShape shapes[] = {{kFew, 16, 64}, {kFew, 16, 32}, {kFew, 16, 16}, {kFew, 32, 32}, {kFew, 32, 64},
+                                     {kFew, 32, 16}, {kFew, 64, 64}, {kFew, 64, 32}, {kFew, 64, 16},
+                                     {kDirect, 16, 4 * kDirectCols}, {kBig, 128, kBN}, {kBig, 256, kBN}};
   const double groups = a.E * (1.0 - std::exp(-double(a.R) / a.E));  // that are touched
-  const double mean = a.R / std::fmax(groups, 1.0);
+  const double mean = a.R / std::fmax(groups, 1.0), bytes = a.K / 2.0 + a.K / 32.0;
   TileShape best = shapes[0];
   double least = 1e300;
   for (const TileShape& s : shapes) {
     const double need = mean / s.rows;
     const double rows = a.E == 1 ? std::ceil(a.R / double(s.rows)) : groups * std::fmax(1.0, need + 0.5);
-    const double cost = std::ceil(std::ceil(rows) * std::ceil(double(a.N) / s.cols) / kCUs) * (s.rows + s.cols);
+    const Cost& c = cost_of_kind[s.kind];
+    const double cost = std::ceil(std::ceil(rows) * std::ceil(double(a.N) / s.cols) / kCUs) *
+                        (c.fixed + (s.rows + s.cols) * bytes / c.rate);
     if (cost < least) {
       least = cost;
       best = s;
@@ -582,15 +841,15 @@ bool plan(const Mx4Args& a, TileShape* s, long* grid) {
   *s = shape_of(a);
   *grid = grid_of(a, *s);
   if (*grid <= max_blocks(kThreads)) return true;
-  *s = {0, 256, kBN};
+  *s = {kBig, 256, kBN};
   *grid = grid_of(a, *s);
   return *grid <= max_blocks(kThreads);
 }
 
 // Rows of a dense product's first launch.  Where the last few rows would make the
 // large tiles go one more round, they go into a launch of their own, in the shape
-// that suits them; a launch counts as much as bringing in kLaunchBytes.
-constexpr double kLaunchBytes = 250e3;
+// that suits them, if that is expected to save the time of a launch.
+constexpr double kLaunchTime = 5;
 int first_rows(const Mx4Args& a) {
   if (a.offsets || a.R <= 256) return a.R;
   const int rows = a.R / 256 * 256;
@@ -602,13 +861,17 @@ int first_rows(const Mx4Args& a) {
   t.R = a.R - rows;
   shape_of(h, &head);
   shape_of(t, &tail);
-  return head + tail + kLaunchBytes / (a.K / 2) < one ? rows : a.R;
+  return head + tail + kLaunchTime < one ? rows : a.R;
 }
 
 hipError_t launch_one(const Mx4Args& a, const TileShape& s, long grid, hipStream_t st) {
   static_assert(kThreads == kFewWaves * 64, "one limit of a launch");
   if (grid == 0) return hipSuccess;
-  if (!s.few) {
+  if (s.kind == kDirect) {
+    hipLaunchKernelGGL((k_mx4_direct<3>), dim3(unsigned(grid)), dim3(kThreads), 0, st, a);
+    return hipGetLastError();
+  }
+  if (s.kind == kBig) {
     if (s.rows == 256) hipLaunchKernelGGL((k_mx4<256>), dim3(unsigned(grid)), dim3(kThreads), 0, st, a);
     else hipLaunchKernelGGL((k_mx4<128>), dim3(unsigned(grid)), dim3(kThreads), 0, st, a);
     return hipGetLastError();
@@ -656,6 +919,40 @@ hipError_t launch_mx4(const Mx4Args& a, hipStream_t st, bool* too_large) {
   if (*too_large) return hipSuccess;
   const hipError_t e = launch_one(head, s, grid, st);
   return e != hipSuccess ? e : launch_one(tail, ts, tail_grid, st);
+}
+
+bool linear_mx4_is_one_launch(int R, int K) { return R <= 1 && K <= kOneMaxK; }
+
+hipError_t launch_linear_mx4_one(const Mx4Args& a, int x_ty, int swiglu, hipStream_t st) {
+  // columns per workgroup: the fewest bytes through a CU
+  int nc = 1;
+  double least = 1e300;
+  for (int c = 2; c >= 1; --c) {
+    const double cost = std::ceil(std::ceil(a.N / (16.0 * c)) / kCUs) * (16 + 16 * c);
+    if (cost < least) {
+      least = cost;
+      nc = c;
+    }
+  }
+  const long tiles = long(a.R) * ((a.N + 16 * nc - 1) / (16 * nc));
+  const unsigned grid = unsigned((tiles + 7) / 8 * 8);
+  if (!grid) return hipSuccess;
+#define MOE_ONE(XT, GLU, NC) hipLaunchKernelGGL((k_mx4_one<XT, GLU, NC>), dim3(grid), dim3(kFewWaves * 64), 0, st, a)
+#define MOE_ONE_NC(XT, GLU)           \
+  do {                                \
+    if (nc == 2) MOE_ONE(XT, GLU, 2); \
+    else MOE_ONE(XT, GLU, 1);         \
+  } while (0)
+  if (x_ty == kBf16) {
+    if (swiglu) MOE_ONE_NC(kBf16, true);
+    else MOE_ONE_NC(kBf16, false);
+  } else {
+    if (swiglu) MOE_ONE_NC(kFp16, true);
+    else MOE_ONE_NC(kFp16, false);
+  }
+#undef MOE_ONE_NC
+#undef MOE_ONE
+  return hipGetLastError();
 }
 
 template <int TY, bool GLU>

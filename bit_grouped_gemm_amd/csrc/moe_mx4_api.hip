@@ -44,7 +44,8 @@ int enqueue(const Mx4Args& a, void* stream) {
 size_t codes_bytes(size_t rows, int K) { return align256(rows * (K / 2)); }
 size_t linear_bytes(const moe_mm_cfg* c, int gathered) {
   const size_t rows = size_t(gathered ? c->T : c->R);
-  return c->R && rows ? codes_bytes(rows, c->K) + align256(rows * (c->K / 32)) : 0;
+  if (linear_mx4_is_one_launch(c->R, c->K)) return 0;
+  return rows ? codes_bytes(rows, c->K) + align256(rows * (c->K / 32)) : 0;
 }
 
 }  // namespace
@@ -91,16 +92,22 @@ extern "C" int moe_linear_mx4(const moe_mm_cfg* cfg, const void* x, int swiglu, 
   const bool some = cfg->R != 0, tokens = some && rows != 0;
   int rc;
   if ((rc = null_ptrs({{x, tokens}, {wq, true}, {ws, true}, {y, some}}))) return rc;
-  if (tokens && !work) return MOE_ERR_NULL_ARG;
+  const bool two = tokens && !linear_mx4_is_one_launch(cfg->R, cfg->K);  // launches, with scratch between them
+  if (two && !work) return MOE_ERR_NULL_ARG;
   if ((rc = check_mm(cfg, offsets, row_token, rows))) return rc;
   if ((rc = check_x(cfg->dtype, swiglu))) return rc;
   if ((rc = misaligned_ptrs({x, wq, ws, y, work}, {offsets, row_token}))) return rc;
-  if (tokens && work_bytes < linear_bytes(cfg, row_token != nullptr)) return MOE_ERR_WORKSPACE;
+  if (two && work_bytes < linear_bytes(cfg, row_token != nullptr)) return MOE_ERR_WORKSPACE;
+  if (some && linear_mx4_is_one_launch(cfg->R, cfg->K)) {
+    Mx4Args a = args_of(cfg, nullptr, nullptr, wq, ws, offsets, row_token, y);
+    a.p = x;
+    return hip_status(launch_linear_mx4_one(a, cfg->dtype, swiglu, static_cast<hipStream_t>(stream)));
+  }
   uint8_t* codes = static_cast<uint8_t*>(work);
-  uint8_t* scales = tokens ? codes + codes_bytes(size_t(rows), cfg->K) : nullptr;
+  uint8_t* scales = two ? codes + codes_bytes(size_t(rows), cfg->K) : nullptr;
   const Mx4Args a = args_of(cfg, codes, scales, wq, ws, offsets, row_token, y);
   if (mx4_too_large(a)) return MOE_ERR_BAD_SHAPE;  // before the quantiser goes out
-  if (tokens && (rc = hip_status(launch_quant_mx4(x, cfg->dtype, swiglu, rows, cfg->K, codes, scales,
+  if (two && (rc = hip_status(launch_quant_mx4(x, cfg->dtype, swiglu, rows, cfg->K, codes, scales,
                                                   static_cast<hipStream_t>(stream)))))
     return rc;
   return enqueue(a, stream);

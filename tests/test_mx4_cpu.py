@@ -74,7 +74,8 @@ def test_linear_workspace():
     size = lambda c, g=0: moe.raw_call("moe_linear_mx4_workspace_size", c, g, C.byref(n))
     assert size(cfg(R=50, K=96)) == moe.MOE_OK and n.value == 2560 + 256
     assert size(cfg(R=5, K=96, T=100), 1) == moe.MOE_OK and n.value == 4864 + 512
-    for kw in (dict(R=0), dict(R=0, T=5), dict(T=0)):
+    assert size(cfg(R=1, K=8224)) == moe.MOE_OK and n.value == 4352 + 512
+    for kw in (dict(R=0), dict(R=0, T=5), dict(T=0), dict(R=1, K=8192), dict(R=1, K=96, T=50)):  # one row: no codes outside the kernel
         assert size(cfg(**kw), int("T" in kw)) == moe.MOE_OK and n.value == 0, kw
     assert size(None) == moe.MOE_ERR_NULL_ARG
     assert moe.raw_call("moe_linear_mx4_workspace_size", cfg(), 0, None) == moe.MOE_ERR_NULL_ARG
