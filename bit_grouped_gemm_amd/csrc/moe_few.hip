@@ -5,10 +5,20 @@
 // with the matrices of expert id[t][j].
 //
 // Bound by the touched experts' weights, which are read once: lanes load matrix
-// fragments straight into registers, several steps ahead, and nothing is shared
+// operands straight into registers, several steps ahead, and nothing is shared
 // between waves but their sums.  h stays exact enough for fp32 results: it is
 // kept as the sum of two 16-bit values, and the second product takes both (the
 // matrix units wait for memory here, so the second half costs nothing).
+//
+// A 16 x 16 x 32 product takes 16 rows of 64 bytes, which is half of each line: the other
+// half then waits in the L1 for the next load, among those of a dozen waves, and is
+// often gone (four steps ahead were slower than two).  So a load has eight rows of 128
+// bytes, and the product's 16 rows are their two halves: row 2 r + s is half s of row r.
+// The other operand is laid out alike, and of the 16 x 16 sums those of equal
+// halves are the ones that are meant; the two of a row are added up at the end.
+//
+// One bf16 token, 8 of 64 experts, H=4096, I=1408: k_up 31 us, 6.0 TB/s of weights, k_down 17,
+// 5.4 (half lines: 40 and 21; a stream of plain reads reaches 6.9 TB/s).  61 tokens: 285 and 170.
 #include "moe_few.h"
 
 #include "moe_mm_tile.h"
@@ -17,7 +27,11 @@
 namespace moe {
 namespace {
 
-constexpr int kRows = kFewTokens;  // rows of a tile: one tile per expert as long as no token names it twice
+// Rows of a tile, for T tokens: the fewest that hold what an expert gets as a rule (a
+// token names it once), as the sums of more would cost every wave the registers that keep
+// its loads in flight.  From 33 tokens on an expert that most of them name has two
+// tiles, and its weights are read twice.
+constexpr int tile_rows(int T) { return T <= 8 ? 8 : T <= 16 ? 16 : 32; }
 constexpr int kStep = 64;          // values of K per step: 128 bytes of a row
 
 template <int TY>
@@ -29,39 +43,40 @@ __device__ __forceinline__ v4f mma16(const v4i& a, const v4i& b, const v4f& c) {
 }
 
 __device__ __forceinline__ v4i load16(const uint16_t* p) { return *reinterpret_cast<const v4i*>(p); }
+// the same of weights: read once, so not kept in the caches
+__device__ __forceinline__ v4i stream16(const uint16_t* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const v4i*>(p));
+}
 
-// The fragments of one step: COLS operands of 16 weight rows, ROWS of 16 rows of
-// the other operand, each in two halves of 32 values.
-template <int COLS, int ROWS>
+// This lane's row of a group of eight, and the first value of its 16 bytes of a step.
+__device__ __forceinline__ int row_of() { return int(threadIdx.x & 15) >> 1; }
+__device__ __forceinline__ int chunk_of() { return 8 * (4 * int(threadIdx.x & 1) + (int(threadIdx.x & 63) >> 4)); }
+
+// One step of NW groups of eight weight rows and NP groups of eight rows of the other operand.
+template <int NW, int NP>
 struct Step {
-  v4i w[COLS][2], p[ROWS][2];
+  v4i w[NW], p[NP];
 };
 
-// acc[i][j] += over the steps [a, b) of K.  Lane l has row l % 16 of each fragment:
-// w[i] and p[j] point to its row's value 8 (l / 16) of step 0; a step's second half lies
-// 32 values on.  D steps are in flight.
-template <int TY, int COLS, int ROWS, int D>
-__device__ __forceinline__ void sum_steps(v4f (&acc)[COLS][ROWS], const uint16_t* const (&w)[COLS],
-                                          const uint16_t* const (&p)[ROWS], int a, int b, int K) {
-  typedef Step<COLS, ROWS> S;
-  const int g = (threadIdx.x & 63) >> 4;
+// acc[i][j] += over the steps [a, b) of K.  Lane l has row (l % 16) / 2 of each group, and of
+// its step the 16 bytes 4 (l % 2) + l / 16; w[i] and p[j] point to them in step 0.  D steps
+// are in flight.
+template <int TY, int NW, int NP, int D>
+__device__ __forceinline__ void sum_steps(v4f (&acc)[NW][NP], const uint16_t* const (&w)[NW],
+                                          const uint16_t* const (&p)[NP], int a, int b, int K) {
+  typedef Step<NW, NP> S;
   const int full = K / kStep, n = min(b, full) - a;  // whole steps
   auto load = [&](S& s, int at) __attribute__((always_inline)) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int i = 0; i < NW; ++i) s.w[i] = stream16(w[i] + long(at) * kStep);
 #pragma unroll
-      for (int i = 0; i < COLS; ++i) s.w[i][h] = load16(w[i] + long(at) * kStep + 32 * h);
-#pragma unroll
-      for (int j = 0; j < ROWS; ++j) s.p[j][h] = load16(p[j] + long(at) * kStep + 32 * h);
-    }
+    for (int j = 0; j < NP; ++j) s.p[j] = load16(p[j] + long(at) * kStep);
   };
   auto use = [&](const S& s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int i = 0; i < NW; ++i)
 #pragma unroll
-      for (int i = 0; i < COLS; ++i)
-#pragma unroll
-        for (int j = 0; j < ROWS; ++j) acc[i][j] = mma16<TY>(s.w[i][h], s.p[j][h], acc[i][j]);
+      for (int j = 0; j < NP; ++j) acc[i][j] = mma16<TY>(s.w[i], s.p[j], acc[i][j]);
   };
   if (n > 0) {
     S s[D];
@@ -81,82 +96,97 @@ __device__ __forceinline__ void sum_steps(v4f (&acc)[COLS][ROWS], const uint16_t
   }
   if (b > full && b > a && K % kStep) {  // the rest of K: zeros behind it
     S s;
+    const bool in = full * kStep + chunk_of() < K;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool in = full * kStep + 32 * h + 8 * g < K;
+    for (int i = 0; i < NW; ++i) s.w[i] = in ? stream16(w[i] + long(full) * kStep) : v4i{0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < COLS; ++i) s.w[i][h] = in ? load16(w[i] + long(full) * kStep + 32 * h) : v4i{0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < ROWS; ++j) s.p[j][h] = in ? load16(p[j] + long(full) * kStep + 32 * h) : v4i{0, 0, 0, 0};
-    }
+    for (int j = 0; j < NP; ++j) s.p[j] = in ? load16(p[j] + long(full) * kStep) : v4i{0, 0, 0, 0};
     use(s);
   }
 }
 
+// The sums of a group of weight rows with a group of the others: lane l has weight
+// rows 2 (l / 16) and 2 (l / 16) + 1 of the other's row (l % 16) / 2.
+__device__ __forceinline__ float2 both_halves(const v4f& acc) {
+  const bool s = threadIdx.x & 1;
+  const float x = s ? acc[1] : acc[0], y = s ? acc[3] : acc[2];
+  return make_float2(x + dpp_f32<0xB1>(x), y + dpp_f32<0xB1>(y));  // (lane xor 1)
+}
+
 // ------------------------------------------------------------------ first product
+// (Steps in flight, us for one token and for 61: 2 31.2 and 290, 3 30.8 and 285, 6 30.6 and 324, 8
+// 35 and 345.)
 constexpr int kUpWaves = 4;
 constexpr int kMaxExperts = 1024;
 
 // 16 columns of h for one row tile: their gate and up rows of W1, K split over the
 // waves, whose sums meet in LDS.
-template <int TY, int NT, int D>
-__device__ __forceinline__ void up_tile(const FewArgs& a, int e, int rows, int i0, const int* list, v4f* part) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, m = lane & 15, g = lane >> 4;
-  const int col = min(i0 + m, a.I - 1);  // (columns behind the last are not stored)
-  const uint16_t* w1 = static_cast<const uint16_t*>(a.w1) + long(e) * 2 * a.I * a.H + 8 * g;
-  const uint16_t* const pw[2] = {w1 + long(col) * a.H, w1 + (long(a.I) + col) * a.H};
-  const uint16_t* px[NT];
+template <int TY, int NP, int D>
+__device__ __forceinline__ void up_tile(const FewArgs& a, int e, int rows, int i0, const int* list, float2* part) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const uint16_t* w1 = static_cast<const uint16_t*>(a.w1) + long(e) * 2 * a.I * a.H + chunk_of();
+  const uint16_t* pw[4];  // eight gate rows, eight more, their up rows
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int r = t * 16 + m;  // (rows behind the last take the first one's values, and are not stored)
-    px[t] = static_cast<const uint16_t*>(a.x) + long(list[r < rows ? r : 0] / a.k) * a.H + 8 * g;
+  for (int i = 0; i < 2; ++i) {
+    const int col = min(i0 + i * 8 + row_of(), a.I - 1);  // (columns behind the last are not stored)
+    pw[i] = w1 + long(col) * a.H;
+    pw[2 + i] = w1 + (long(a.I) + col) * a.H;
   }
-  v4f acc[2][NT];
+  const uint16_t* px[NP];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) acc[0][t] = acc[1][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int j = 0; j < NP; ++j) {
+    const int r = j * 8 + row_of();  // (rows behind the last take the first one's values, and are not stored)
+    px[j] = static_cast<const uint16_t*>(a.x) + long(list[r < rows ? r : 0] / a.k) * a.H + chunk_of();
+  }
+  v4f acc[4][NP];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < NP; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   const int steps = (a.H + kStep - 1) / kStep;
-  sum_steps<TY, 2, NT, D>(acc, pw, px, w * steps / kUpWaves, (w + 1) * steps / kUpWaves, a.H);
+  sum_steps<TY, 4, NP, D>(acc, pw, px, w * steps / kUpWaves, (w + 1) * steps / kUpWaves, a.H);
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int t = 0; t < NT; ++t) part[((w * 2 + c) * NT + t) * 64 + lane] = acc[c][t];
+    for (int j = 0; j < NP; ++j) part[((w * 4 + i) * NP + j) * 64 + lane] = both_halves(acc[i][j]);
   __syncthreads();
-  if (w < NT) {  // fragment w: lane l holds columns 4 (l / 16) + 0..3 of row l % 16
-    v4f s[2];
+  for (int f = w; f < 2 * NP; f += kUpWaves) {  // eight columns of eight rows
+    const int i = f / NP, j = f % NP;
+    float2 gate = {0.0f, 0.0f}, up = {0.0f, 0.0f};
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      s[c] = part[(c * NT + w) * 64 + lane];
-#pragma unroll
-      for (int u = 1; u < kUpWaves; ++u) s[c] += part[((u * 2 + c) * NT + w) * 64 + lane];
+    for (int u = 0; u < kUpWaves; ++u) {
+      const float2 g = part[((u * 4 + i) * NP + j) * 64 + lane], v = part[((u * 4 + 2 + i) * NP + j) * 64 + lane];
+      gate.x += g.x;
+      gate.y += g.y;
+      up.x += v.x;
+      up.y += v.y;
     }
-    const int r = w * 16 + m, c = i0 + 4 * g;
-    if (r < rows && c < a.I) {
-      v4f hi, lo;
-      uint2 top;
+    const int r = j * 8 + row_of(), c = i0 + i * 8 + 2 * (lane >> 4);
+    if (r >= rows || c >= a.I || (lane & 1)) continue;
+    const v4f h = {swiglu(gate.x, up.x), swiglu(gate.y, up.y), 0.0f, 0.0f};
+    const uint32_t hi = round4(h, TY).x;
+    v4f lo = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) hi[j] = swiglu(s[0][j], s[1][j]);
-      top = round4(hi, TY);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t bits = (j < 2 ? top.x : top.y) >> (16 * (j & 1)) & 0xFFFFu;
-        const float back = TY == kBf16 ? bf16_to_f32(bits) : float(__builtin_bit_cast(_Float16, uint16_t(bits)));
-        lo[j] = fabsf(back) < __builtin_inff() ? hi[j] - back : 0.0f;  // (past the type's range: infinity)
-      }
-      const long at = long(list[r]) * a.I + c;
-      *reinterpret_cast<uint2*>(a.hi + at) = top;
-      *reinterpret_cast<uint2*>(a.lo + at) = round4(lo, TY);
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t bits = hi >> (16 * u) & 0xFFFFu;
+      const float back = TY == kBf16 ? bf16_to_f32(bits) : float(__builtin_bit_cast(_Float16, uint16_t(bits)));
+      lo[u] = fabsf(back) < __builtin_inff() ? h[u] - back : 0.0f;  // (past the type's range: infinity)
     }
+    const long at = long(list[r]) * a.I + c;
+    *reinterpret_cast<uint32_t*>(a.hi + at) = hi;
+    *reinterpret_cast<uint32_t*>(a.lo + at) = round4(lo, TY).x;
   }
 }
 
 // A workgroup finds its row tile from the routing result itself: experts' counts,
 // then the tile's expert, then its slots in their order.  The workgroups of the
 // first columns write that down for the second launch.
-template <int TY>
+template <int TY, int MAXP>
 __global__ __launch_bounds__(kUpWaves * 64) void k_up(FewArgs a, int ncol) {
+  constexpr int kRows = 8 * MAXP;
   __shared__ int hist[kMaxExperts];
   __shared__ int list[kRows];
-  __shared__ v4f part[kUpWaves * 2 * (kRows / 16) * 64];
+  __shared__ float2 part[kUpWaves * 4 * MAXP * 64];
   const int lane = threadIdx.x & 63, n = a.T * a.k;
   const int want = int(blockIdx.x) / ncol, ct = int(blockIdx.x) - want * ncol;
   for (int e = threadIdx.x; e < a.E; e += kUpWaves * 64) hist[e] = 0;
@@ -203,51 +233,60 @@ __global__ __launch_bounds__(kUpWaves * 64) void k_up(FewArgs a, int ncol) {
     if (notes && lane == 0) a.tiles[want] = make_int2(e, rows);
   }
   __syncthreads();
-  if (rows <= 16) up_tile<TY, 1, 4>(a, e, rows, ct * 16, list, part);
-  else if (rows <= 32) up_tile<TY, 2, 3>(a, e, rows, ct * 16, list, part);
-  else up_tile<TY, 4, 2>(a, e, rows, ct * 16, list, part);
+  if (MAXP == 1 || rows <= 8) up_tile<TY, 1, 3>(a, e, rows, ct * 16, list, part);
+  else if (MAXP == 2 || rows <= 16) up_tile<TY, MAXP < 2 ? MAXP : 2, 2>(a, e, rows, ct * 16, list, part);
+  else up_tile<TY, MAXP, 2>(a, e, rows, ct * 16, list, part);
 }
 
 // ------------------------------------------------------------------ second product
+// (Steps in flight, us for one token and for 61: 4 16.9 and 170, 6 16.8 and 170, 8 16.8 and 169; 16 waves
+// with 4: 17.1 and 179.)
 constexpr int kDownWaves = 8;
 
-// Steps [s0, s1) of row tile v for 16 columns of out, added to the wave's own sums
+// Steps [s0, s1) of a row tile for 16 columns of out, added to the wave's own sums
 // by token.
-template <int TY, int NT, int D>
-__device__ __forceinline__ void down_tile(const FewArgs& a, int v, int e, int rows, int n0, int s0, int s1,
+template <int TY, int NP, int D>
+__device__ __forceinline__ void down_tile(const FewArgs& a, const int32_t* slots, int e, int rows, int n0, int s0, int s1,
                                           float (*sums)[16]) {
-  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
-  const int col = min(n0 + m, a.H - 1);
-  const uint16_t* const pw[1] = {static_cast<const uint16_t*>(a.w2) + (long(e) * a.H + col) * a.I + 8 * g};
-  const uint16_t* ph[2 * NT];
-  int slot[NT];
+  const int lane = threadIdx.x & 63;
+  const uint16_t* w2 = static_cast<const uint16_t*>(a.w2) + long(e) * a.H * a.I + chunk_of();
+  const uint16_t* pw[2];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int r = t * 16 + m;
-    slot[t] = a.slots[v * kRows + (r < rows ? r : 0)];
-    ph[t] = a.hi + long(slot[t]) * a.I + 8 * g;
-    ph[NT + t] = a.lo + long(slot[t]) * a.I + 8 * g;
+  for (int i = 0; i < 2; ++i) pw[i] = w2 + long(min(n0 + i * 8 + row_of(), a.H - 1)) * a.I;
+  const uint16_t* ph[2 * NP];
+  int slot[NP];
+#pragma unroll
+  for (int j = 0; j < NP; ++j) {
+    const int r = j * 8 + row_of();
+    slot[j] = slots[r < rows ? r : 0];
+    ph[j] = a.hi + long(slot[j]) * a.I + chunk_of();
+    ph[NP + j] = a.lo + long(slot[j]) * a.I + chunk_of();
   }
-  v4f acc[1][2 * NT];
+  v4f acc[2][2 * NP];
 #pragma unroll
-  for (int t = 0; t < 2 * NT; ++t) acc[0][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  sum_steps<TY, 1, 2 * NT, D>(acc, pw, ph, s0, s1, a.I);
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    if (t * 16 + m < rows) {
-      const float weight = a.weights[slot[t]];
-      float* to = sums[slot[t] / a.k] + 4 * g;
+    for (int j = 0; j < 2 * NP; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  sum_steps<TY, 2, 2 * NP, D>(acc, pw, ph, s0, s1, a.I);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)  // (two rows of a tile may be one token's)
-        __hip_atomic_fetch_add(to + j, weight * (acc[0][t][j] + acc[0][NT + t][j]), __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_WORKGROUP);
+  for (int j = 0; j < NP; ++j) {
+    const bool mine = j * 8 + row_of() < rows && !(lane & 1);
+    const float weight = mine ? a.weights[slot[j]] : 0.0f;
+    float* to = sums[slot[j] / a.k] + 2 * (lane >> 4);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 y = both_halves(acc[i][j] + acc[i][NP + j]);
+      if (mine) {  // (two rows of a tile may be one token's)
+        __hip_atomic_fetch_add(to + i * 8, weight * y.x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        __hip_atomic_fetch_add(to + i * 8 + 1, weight * y.y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+      }
     }
   }
 }
 
 // 16 columns of out: all steps of all row tiles in one row, an eighth of them to
 // each wave.
-template <int TY>
+template <int TY, int MAXP>
 __global__ __launch_bounds__(kDownWaves * 64) void k_down(FewArgs a) {
   __shared__ float sums[kDownWaves][kFewTokens][16];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = int(blockIdx.x) * 16;
@@ -259,9 +298,10 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_down(FewArgs a) {
   while (at < end) {
     const int v = int(at / each), s0 = int(at - long(v) * each), s1 = int(min(long(each), s0 + end - at));
     const int2 tile = a.tiles[v];
-    if (tile.y <= 16) down_tile<TY, 1, 4>(a, v, tile.x, tile.y, n0, s0, s1, sums[w]);
-    else if (tile.y <= 32) down_tile<TY, 2, 2>(a, v, tile.x, tile.y, n0, s0, s1, sums[w]);
-    else down_tile<TY, 4, 1>(a, v, tile.x, tile.y, n0, s0, s1, sums[w]);
+    const int32_t* slots = a.slots + v * 8 * MAXP;
+    if (MAXP == 1 || tile.y <= 8) down_tile<TY, 1, 6>(a, slots, tile.x, tile.y, n0, s0, s1, sums[w]);
+    else if (MAXP == 2 || tile.y <= 16) down_tile<TY, MAXP < 2 ? MAXP : 2, 4>(a, slots, tile.x, tile.y, n0, s0, s1, sums[w]);
+    else down_tile<TY, MAXP, 2>(a, slots, tile.x, tile.y, n0, s0, s1, sums[w]);
     at += s1 - s0;
   }
   __syncthreads();
@@ -276,27 +316,37 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_down(FewArgs a) {
 
 // Row tiles at most: each expert has one more than it fills.
 long most_tiles(int T, int E, int k) {
-  const long n = long(T) * k, most = (E < n ? E : n) + n / kRows;
+  const long n = long(T) * k, most = (E < n ? E : n) + n / tile_rows(T);
   return most < n ? most : n;
 }
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
-template <int TY>
-hipError_t launch_ty(const FewArgs& a, hipStream_t st) {
+template <int TY, int MAXP>
+hipError_t launch_rows(const FewArgs& a, hipStream_t st) {
   const int ncol = (a.I + 15) / 16;
-  hipLaunchKernelGGL((k_up<TY>), dim3(unsigned(most_tiles(a.T, a.E, a.k) * ncol)), dim3(kUpWaves * 64), 0, st, a, ncol);
+  hipLaunchKernelGGL((k_up<TY, MAXP>), dim3(unsigned(most_tiles(a.T, a.E, a.k) * ncol)), dim3(kUpWaves * 64), 0, st, a,
+                     ncol);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_down<TY>), dim3(unsigned((a.H + 15) / 16)), dim3(kDownWaves * 64), 0, st, a);
+  hipLaunchKernelGGL((k_down<TY, MAXP>), dim3(unsigned((a.H + 15) / 16)), dim3(kDownWaves * 64), 0, st, a);
   return hipGetLastError();
+}
+
+template <int TY>
+hipError_t launch_ty(const FewArgs& a, hipStream_t st) {
+  switch (tile_rows(a.T)) {
+    case 8: return launch_rows<TY, 1>(a, st);
+    case 16: return launch_rows<TY, 2>(a, st);
+    default: return launch_rows<TY, 4>(a, st);
+  }
 }
 
 }  // namespace
 
 size_t few_bytes(int T, int I, int E, int k) {
   const size_t tiles = size_t(most_tiles(T, E, k));
-  return 256 + up256(tiles * sizeof(int2)) + up256(tiles * kRows * 4) + 2 * up256(size_t(T) * k * I * 2);
+  return 256 + up256(tiles * sizeof(int2)) + up256(tiles * tile_rows(T) * 4) + 2 * up256(size_t(T) * k * I * 2);
 }
 
 void few_carve(FewArgs& a, void* ws) {
@@ -307,7 +357,7 @@ void few_carve(FewArgs& a, void* ws) {
   a.tiles = reinterpret_cast<int2*>(p);
   p += up256(tiles * sizeof(int2));
   a.slots = reinterpret_cast<int32_t*>(p);
-  p += up256(tiles * kRows * 4);
+  p += up256(tiles * tile_rows(a.T) * 4);
   a.hi = reinterpret_cast<uint16_t*>(p);
   p += up256(size_t(a.T) * a.k * a.I * 2);
   a.lo = reinterpret_cast<uint16_t*>(p);
