@@ -38,6 +38,7 @@ from __future__ import annotations
 
 import ctypes as C
 import dataclasses
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -787,6 +788,38 @@ def moe_linear_i8(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets: 
     return out
 
 
+def _beside(name, given, like):
+    """An output of a checked operand's own kind and its address: a new one, or the caller's."""
+    if given is None:
+        out = torch.empty_like(like)
+        return out, out.data_ptr() or None
+    return given, _addr(name, given, (like.dtype,), like.shape, like.device)
+
+
+# The calls' structs, by their values: put together once per shape.
+@functools.lru_cache(maxsize=1024)
+def _mm_cfg(*values):
+    return C.byref(MoeMmCfg(*values))
+
+
+@functools.lru_cache(maxsize=1024)
+def _few_cfg(*values):
+    return C.byref(MoeFewCfg(*values))
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_cfg(*values):
+    return C.byref(MoeNormCfg(*values))
+
+
+@functools.lru_cache(maxsize=1024)
+def _scratch_bytes(name: str, cfg, *more) -> int:
+    """The workspace size that entry point `name` gives for a cached struct."""
+    n = C.c_size_t(0)
+    _check(name, getattr(_lib or load(), name)(cfg, *more, C.byref(n)))
+    return n.value
+
+
 # ------------------------------------------------------------------ row-major MXFP4
 def moe_quant_mx4(x: torch.Tensor, swiglu: bool = False, codes: Optional[torch.Tensor] = None,
                   scales: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -852,25 +885,19 @@ def moe_mm_mx4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.T
     given = out
     out, clear = _new_or_checked(out, (R, N), out_dtype or torch.bfloat16, tuple(_DT), xq)
     py = _addr("out", out, tuple(_DT), (R, N), dev)
-    c = MoeMmCfg(R, N, K, E, T, 0, _DT[out.dtype], clear)
-    _call("moe_mm_mx4", dev.index, C.byref(c), pq, ps, pw, pws, po, pt, py)
+    c = _mm_cfg(R, N, K, E, T, 0, _DT[out.dtype], clear)
+    _call("moe_mm_mx4", dev.index, c, pq, ps, pw, pws, po, pt, py)
     if given is not None:
         _written(given)
     return out
 
 
-def _linear_mx4_bytes(c: MoeMmCfg, gathered: int) -> int:
-    n = C.c_size_t(0)
-    _check("moe_linear_mx4_workspace_size",
-           (_lib or load()).moe_linear_mx4_workspace_size(C.byref(c), gathered, C.byref(n)))
-    return n.value
-
-
 def moe_linear_mx4_workspace_size(rows: int, K: int, out_rows: Optional[int] = None) -> int:
     """Bytes of scratch moe_linear_mx4 needs for x of `rows` rows, K inputs of w
     and, with row_token, `out_rows` rows of the result."""
-    return _linear_mx4_bytes(MoeMmCfg(rows if out_rows is None else out_rows, 8, K, 1, rows, 0, 0, 0),
-                             int(out_rows is not None))
+    return _scratch_bytes("moe_linear_mx4_workspace_size",
+                          _mm_cfg(rows if out_rows is None else out_rows, 8, K, 1, rows, 0, 0, 0),
+                          int(out_rows is not None))
 
 
 def moe_linear_mx4(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets: Optional[torch.Tensor] = None,
@@ -891,12 +918,12 @@ def moe_linear_mx4(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets:
     given = out
     out, clear = _new_or_checked(out, (R, N), out_dtype or x.dtype, tuple(_DT), x)
     py = _addr("out", out, tuple(_DT), (R, N), dev)
-    c = MoeMmCfg(R, N, K, E, T, _DT[x.dtype], _DT[out.dtype], clear)
+    c = _mm_cfg(R, N, K, E, T, _DT[x.dtype], _DT[out.dtype], clear)
     if work is None:
-        need = _linear_mx4_bytes(c, int(row_token is not None))
+        need = _scratch_bytes("moe_linear_mx4_workspace_size", c, int(row_token is not None))
         work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     pk = None if work is None else _addr("work", work, (torch.uint8,), work.shape, dev)
-    _call("moe_linear_mx4", dev.index, C.byref(c), px, int(bool(swiglu)), pw, pws, po, pt, py, pk,
+    _call("moe_linear_mx4", dev.index, c, px, int(bool(swiglu)), pw, pws, po, pt, py, pk,
           0 if work is None else work.numel())
     if given is not None:
         _written(given)
@@ -904,15 +931,9 @@ def moe_linear_mx4(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets:
 
 
 # ------------------------------------------------------------------ the layer for a few tokens
-def _few_bytes(c: MoeFewCfg) -> int:
-    n = C.c_size_t(0)
-    _check("moe_layer_mm_workspace_size", (_lib or load()).moe_layer_mm_workspace_size(C.byref(c), C.byref(n)))
-    return n.value
-
-
 def moe_layer_mm_workspace_size(T: int, H: int, I: int, E: int, topk: int) -> int:
     """Bytes of scratch moe_layer_mm needs for T tokens."""
-    return _few_bytes(MoeFewCfg(T, H, I, E, topk, 0))
+    return _scratch_bytes("moe_layer_mm_workspace_size", _few_cfg(T, H, I, E, topk, 0))
 
 
 def moe_layer_mm(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor, w1: torch.Tensor,
@@ -943,15 +964,15 @@ def moe_layer_mm(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Te
     p1 = _addr("w1", w1, (dt,), (E, two, H), dev)
     p2 = _addr("w2", w2, (dt,), (E, H, I), dev)
     given = out
-    if out is None:
-        out = torch.empty_like(x)
-    po = _addr("out", out, (dt,), (T, H), dev)
-    c = MoeFewCfg(T, H, I, E, topk, _DT[dt])
+    out, po = _beside("out", out, x)
+    c = _few_cfg(T, H, I, E, topk, _DT[dt])
     if ws is None:
-        need = _few_bytes(c)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    pk = None if ws is None else _addr("ws", ws, (torch.uint8,), ws.shape, dev)
-    _call("moe_layer_mm", dev.index, C.byref(c), px, pi, pt, p1, p2, po, pk, 0 if ws is None else ws.numel())
+        nb = _scratch_bytes("moe_layer_mm_workspace_size", c)
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        pk = ws.data_ptr() or None
+    else:
+        pk, nb = _addr("ws", ws, (torch.uint8,), ws.shape, dev), ws.numel()
+    _call("moe_layer_mm", dev.index, c, px, pi, pt, p1, p2, po, pk, nb)
     if given is not None:
         _written(given)
     return out
@@ -964,13 +985,7 @@ def _norm_operands(x, weight, residual, eps, fmt=0, group=0):
     px = _addr("x", x, _16BIT, (R, K), dev)
     pr = None if residual is None else _addr("residual", residual, (dt,), (R, K), dev)
     pw = _addr("weight", weight, (dt, torch.float32), (K,), dev)
-    return MoeNormCfg(R, K, _DT[dt], _DT[weight.dtype], fmt, group, eps), R, K, px, pr, pw
-
-
-def _beside(name, given, like):
-    """An output of the operand's own kind: a new one, or the caller's."""
-    out = torch.empty_like(like) if given is None else given
-    return out, _addr(name, out, (like.dtype,), like.shape, like.device)
+    return _norm_cfg(R, K, _DT[dt], _DT[weight.dtype], fmt, group, eps), R, K, px, pr, pw
 
 
 def _rms_norm(x, weight, residual, eps, out=None, sum_out=None, want_rstd=False):
@@ -983,7 +998,7 @@ def _rms_norm(x, weight, residual, eps, out=None, sum_out=None, want_rstd=False)
             raise ValueError("out and sum_out are the same tensor")
     if want_rstd:
         rstd = torch.empty(R, dtype=torch.float32, device=x.device)
-    _call("moe_rms_norm", x.device.index, C.byref(c), px, pr, pw, py, ps,
+    _call("moe_rms_norm", x.device.index, c, px, pr, pw, py, ps,
           None if rstd is None else rstd.data_ptr() or None)
     for t in (out, sum_out if residual is not None else None):
         if t is not None:
@@ -1020,13 +1035,6 @@ def _usable(dy):
     return dy.clone() if dy.data_ptr() % 16 else dy
 
 
-def _norm_bytes(c: MoeNormCfg) -> int:
-    n = C.c_size_t(0)
-    _check("moe_rms_norm_backward_workspace_size",
-           (_lib or load()).moe_rms_norm_backward_workspace_size(C.byref(c), C.byref(n)))
-    return n.value
-
-
 def _rms_norm_backward(dy, dsum, s, rstd, weight, eps, dx, dw, work):
     (R, K), dt, dev = _rows_of("dy", dy), dy.dtype, dy.device
     pd = _addr("dy", dy, _16BIT, (R, K), dev)
@@ -1036,18 +1044,18 @@ def _rms_norm_backward(dy, dsum, s, rstd, weight, eps, dx, dw, work):
     pw = _addr("weight", weight, (dt, torch.float32), (K,), dev)
     px = None if dx is None else _addr("dx", dx, (dt,), (R, K), dev)
     pdw = None if dw is None else _addr("dweight", dw, (weight.dtype,), (K,), dev)
-    c = MoeNormCfg(R, K, _DT[dt], _DT[weight.dtype], 0, 0, eps)
+    c = _norm_cfg(R, K, _DT[dt], _DT[weight.dtype], 0, 0, eps)
     if work is None and dw is not None:
-        need = _norm_bytes(c)
+        need = _scratch_bytes("moe_rms_norm_backward_workspace_size", c)
         work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     pk = None if work is None else _addr("work", work, (torch.uint8,), work.shape, dev)
-    _call("moe_rms_norm_backward", dev.index, C.byref(c), pd, pg, ps, pr, pw, px, pdw, pk,
+    _call("moe_rms_norm_backward", dev.index, c, pd, pg, ps, pr, pw, px, pdw, pk,
           0 if work is None else work.numel())
 
 
 def moe_rms_norm_backward_workspace_size(R: int, K: int) -> int:
     """Bytes of scratch moe_rms_norm_backward needs for the gradient of the weight."""
-    return _norm_bytes(MoeNormCfg(R, K, 0, 0, 0, 0, 1.0))
+    return _scratch_bytes("moe_rms_norm_backward_workspace_size", _norm_cfg(R, K, 0, 0, 0, 0, 1.0))
 
 
 def moe_rms_norm_backward(dy: torch.Tensor, dsum: Optional[torch.Tensor], sum: torch.Tensor, rstd: torch.Tensor,
@@ -1121,7 +1129,7 @@ def moe_rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional
     else:
         codes = torch.empty(R, K, dtype=torch.uint8, device=dev)
         scales = torch.empty(R, K // max(group, 1), dtype=torch.float32, device=dev)
-    _call("moe_rms_norm_quant", dev.index, C.byref(c), px, pr, pw, py, ps, codes.data_ptr() or None,
+    _call("moe_rms_norm_quant", dev.index, c, px, pr, pw, py, ps, codes.data_ptr() or None,
           scales.data_ptr() or None)
     if s is not None and sum_out is not None:
         _written(sum_out)
