@@ -105,6 +105,7 @@ __device__ __forceinline__ uint32_t row_top(uint32_t v, uint32_t* slot) {
 constexpr float kTiny = 0x1p-80f;  // keeps the squares of any finite row's values, and their sum, inside fp32
 
 // THREADS lanes per row (64: four rows per workgroup), NC chunks of 8 values a lane.
+// Bound by HBM: 8 bytes a value with the residual, 16384 rows of 4096: 94 us, 5.7 TB/s.
 template <int TY, int FMT, int THREADS, int NC>
 __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void k_norm(NormArgs a) {
   constexpr int kRows = THREADS < 256 ? 256 / THREADS : 1;
@@ -207,14 +208,17 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void k_norm(NormArgs
 // ------------------------------------------------------------------ gradients
 // Workgroups of the backward pass; each takes every so-many-th row and keeps
 // its part of dweight in registers.
-constexpr int kGradBlocks = 512;
+// (us, 16384 rows of 4096: 512 of 256 lanes 104, 512 of 512 105, 256 of 1024 102; 4099 of 7168: 57, 52,
+// 50; 1024 of 4096: 16.5, 15.7, 14.1; twice as many are slower everywhere.)
 int grad_rows(int K) { return K <= 1024 ? 4 : 1; }  // rows a workgroup has at a time
 int grad_blocks(int R, int K) {
-  const int n = grad_rows(K);
+  const int n = grad_rows(K), most = K <= 2048 ? 512 : 256;
   const long need = (long(R) + n - 1) / n;
-  return int(need < kGradBlocks ? need : kGradBlocks);
+  return int(need < most ? need : most);
 }
 
+// Bound by HBM: 8 bytes a value with the sum's gradient; 16384 rows of 4096: 102 us with the
+// join, 5.3 TB/s.
 template <int TY, int THREADS, int NC>
 __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void k_norm_grad(NormGradArgs a) {
   constexpr int kRows = THREADS < 256 ? 256 / THREADS : 1;
@@ -334,13 +338,16 @@ hipError_t launch_rows(const NormArgs& all, hipStream_t st) {
   return hipSuccess;
 }
 
+// Lanes and chunks: a wave per row up to 1024 values, a workgroup from there on.  (With the
+// residual, us: 16384 rows of 1024 in 64 x 2 26.0, 256 x 1 29.8; 16384 of 4096 in 256 x 2 99.8, 512
+// x 1 96.4, 512 x 2 93.7, 1024 x 1 103.5; 4099 of 7168 in 256 x 4 50.2, 512 x 2 41.6, 1024 x 1 41.8; 61
+// of 7168 4.8, 3.3, 3.1.)
 template <int TY, int FMT>
 hipError_t launch_fmt(const NormArgs& a, hipStream_t st) {
   if (a.K <= 512) return launch_rows<TY, FMT, 64, 1>(a, st);
   if (a.K <= 1024) return launch_rows<TY, FMT, 64, 2>(a, st);
   if (a.K <= 2048) return launch_rows<TY, FMT, 256, 1>(a, st);
-  if (a.K <= 4096) return launch_rows<TY, FMT, 256, 2>(a, st);
-  if (a.K <= 8192) return launch_rows<TY, FMT, 256, 4>(a, st);
+  if (a.K <= 8192) return launch_rows<TY, FMT, 512, 2>(a, st);
   return launch_rows<TY, FMT, 512, 4>(a, st);
 }
 
@@ -363,9 +370,8 @@ hipError_t launch_grad(const NormGradArgs& a, hipStream_t st) {
     if (a.K <= 512) MOE_GRAD(64, 1);
     else if (a.K <= 1024) MOE_GRAD(64, 2);
     else if (a.K <= 2048) MOE_GRAD(256, 1);
-    else if (a.K <= 4096) MOE_GRAD(256, 2);
-    else if (a.K <= 8192) MOE_GRAD(256, 4);
-    else MOE_GRAD(512, 4);
+    else if (a.K <= 8192) MOE_GRAD(1024, 1);
+    else MOE_GRAD(1024, 2);
 #undef MOE_GRAD
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
