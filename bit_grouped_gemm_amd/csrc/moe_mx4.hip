@@ -88,13 +88,20 @@ __device__ __forceinline__ int token_of(const Mx4Args& a, int row) {
   return t >= 0 && t < a.T ? t : -1;
 }
 
-// Where there are too few tiles for the chip: a workgroup makes 16 NC columns by
-// 16 NT rows; each of its four waves takes a quarter of the K steps through a
-// ring of S stages of its own, and their sums are added up, in the order of the
-// waves, through LDS.
+// A wave makes 16 NC columns by 16 NT rows, its weights' and rows' K steps coming through
+// a ring of S stages of its own, so nothing waits for another wave.
+//   WK = 4: the four waves of a workgroup have the same columns, and a quarter of the steps
+//     each; their sums are added up, in the order of the waves, through LDS.  Where
+//     there are too few tiles for the chip.
+//   WK = 1: each has columns of its own and all steps.  Where there are many tiles of few
+//     rows (a decode batch's experts): nothing to join, and loads that never pause.
+// Bound by the weights' bytes.  S is 2, which lets the most workgroups share a CU; but for
+// 16 x 16 tiles, which as a rule have a CU to themselves.  (61 tokens, top-8 of 64, us: 7168 ->
+// 2048 75, 6.7 TB/s of weights, with four stages 78, as four quarters 113; 2048 -> 7168 84,
+// 6.0 TB/s.)
 constexpr int kFewWaves = 4;
 
-template <int NC, int NT, int S>
+template <int NC, int NT, int S, int WK>
 __global__ __launch_bounds__(kFewWaves * 64) void k_mx4_few(Mx4Args a) {
   constexpr int L = 2 * (NC + NT);            // loads of a wave per step
   constexpr int kStage = L * 1024;            // bytes of a wave's stage
@@ -112,15 +119,17 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_mx4_few(Mx4Args a) {
   static_assert(kGroupSteps % S == 0, "the loop takes whole groups");
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, g = lane >> 4;
-  const int ncol = (a.N + 16 * NC - 1) / (16 * NC);
+  constexpr int kCols = 16 * NC * (kFewWaves / WK);
+  const int ncol = (a.N + kCols - 1) / kCols;
   Place pl;
   int ct;
   if (!find_tile(a, 16 * NT, ncol, blockIdx.x, pl, ct)) return;
   const int ld = a.K / 2, nb = a.K / 32;  // bytes of codes and of scales per row of both operands
-  const int n0 = ct * 16 * NC;
+  const int n0 = ct * kCols + (WK == 1 ? w * 16 * NC : 0);
+  if (n0 >= a.N) return;  // (WK = 4: of no wave)
   const int steps = pl.e >= a.E ? 0 : (ld + 127) / 128;
-  const int each = (steps + kFewWaves - 1) / kFewWaves;
-  const int s0 = w * each, mine = max(0, min(steps - s0, each));
+  const int each = (steps + WK - 1) / WK;
+  const int s0 = WK == 1 ? 0 : w * each, mine = max(0, min(steps - s0, each));
 
   const uint8_t* wq = static_cast<const uint8_t*>(a.q) + (long(pl.e) * a.N + n0) * ld;
   const int wrows = min(16 * NC, a.N - n0);
@@ -245,133 +254,33 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_mx4_few(Mx4Args a) {
     }
   }
 
-  stage_barrier();  // every load has landed: the first stage takes the sums
-  v4f* part = reinterpret_cast<v4f*>(st0);
-#pragma unroll
-  for (int i = 0; i < NC; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) part[(w * NC * NT + i * NT + j) * 64 + lane] = acc[i][j];
-  __syncthreads();
-  // fragment f's sum by wave f % 4: lane l holds columns 4 (l / 16) + 0..3 of row l % 16
-  for (int f = w; f < NC * NT; f += kFewWaves) {
-    v4f sum = part[f * 64 + lane];
-#pragma unroll
-    for (int v = 1; v < kFewWaves; ++v) sum += part[(v * NC * NT + f) * 64 + lane];
-    const int r = (f % NT) * 16 + m, c = n0 + (f / NT) * 16 + 4 * g;
-    if (r >= pl.rows || c >= a.N) continue;
+  // fragment (i, j): lane l holds columns 4 (l / 16) + 0..3 of row l % 16
+  auto put_out = [&](int i, int j, v4f sum) __attribute__((always_inline)) {
+    const int r = j * 16 + m, c = n0 + i * 16 + 4 * g;
+    if (r >= pl.rows || c >= a.N) return;
     if (pl.e < a.E && token_of(a, pl.row0 + r) < 0) sum = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     store4(a.out, (long(pl.row0) + r) * a.N + c, sum, a.out_ty);
-  }
-}
-
-// Many small groups (a decode batch's experts): 16 rows by 64 columns per wave, all of K,
-// nothing shared between the four waves of a workgroup but their rows.  Lanes load
-// matrix fragments straight into registers, D steps ahead, so there is no stage to
-// fill and no sum to join.  Bound by the weights' bytes: 61 tokens, top-8 of 64, 2048 ->
-// 7168: 106 us, 4.7 TB/s of weights, where k_mx4_few takes 147.
-constexpr int kDirectCols = 64;  // of a wave
-
-template <int D>
-__global__ __launch_bounds__(256) void k_mx4_direct(Mx4Args a) {
-  constexpr int NC = kDirectCols / 16;
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int m = lane & 15, g = lane >> 4;
-  const int ncol = (a.N + 4 * kDirectCols - 1) / (4 * kDirectCols);
-  Place pl;
-  int ct;
-  if (!find_tile(a, 16, ncol, blockIdx.x, pl, ct)) return;
-  const int n0 = (ct * 4 + w) * kDirectCols, ld = a.K / 2, nb = a.K / 32;
-  if (n0 >= a.N) return;
-  const bool grouped = pl.e < a.E;
-  const int t = m < pl.rows ? token_of(a, pl.row0 + m) : 0;
-  v4f acc[NC];
+  };
+  if constexpr (WK == 1) {
 #pragma unroll
-  for (int i = 0; i < NC; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  if (grouped) {
-    // Lane l has row l % 16 of each fragment, bytes 64 h + 16 (l / 16) + 0..15 of half h of a step.
-    // Columns and rows behind the last, and rows that name no token, take the values of
-    // one that is there: their results are not stored, or stored as zeros.
-    const uint8_t *pw[NC], *qe[NC];
+    for (int i = 0; i < NC; ++i)
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const long row = long(pl.e) * a.N + min(n0 + i * 16 + m, a.N - 1);
-      pw[i] = static_cast<const uint8_t*>(a.q) + row * ld + 16 * g;
-      qe[i] = a.qe + row * nb;
+      for (int j = 0; j < NT; ++j) put_out(i, j, acc[i][j]);
+    wait_vm<0>();  // no load is on its way into LDS that another workgroup may get
+  } else {
+    stage_barrier();  // every load has landed: the first stage takes the sums
+    v4f* part = reinterpret_cast<v4f*>(st0);
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) part[(w * NC * NT + i * NT + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    for (int f = w; f < NC * NT; f += kFewWaves) {  // fragment f's sum by wave f % 4
+      v4f sum = part[f * 64 + lane];
+#pragma unroll
+      for (int v = 1; v < kFewWaves; ++v) sum += part[(v * NC * NT + f) * 64 + lane];
+      put_out(f / NT, f % NT, sum);
     }
-    const bool none = a.row_token && a.T == 0;
-    const long row = none ? 0 : a.row_token ? max(t, 0) : pl.row0 + (m < pl.rows ? m : 0);
-    const uint8_t* pp = static_cast<const uint8_t*>(none ? a.q : a.p) + row * ld + 16 * g;
-    const uint8_t* pe = (none ? a.qe : a.pe) + row * nb;
-    struct Step {
-      v4i w[NC][2], p[2];
-      uint2 qe[NC], pe;  // the eight scales of the row's step
-    };
-    auto load = [&](Step& s, int at) __attribute__((always_inline)) {
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) s.w[i][h] = *reinterpret_cast<const v4i*>(pw[i] + at * 128 + 64 * h);
-        __builtin_memcpy(&s.qe[i], qe[i] + at * 8, 8);
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) s.p[h] = *reinterpret_cast<const v4i*>(pp + at * 128 + 64 * h);
-      __builtin_memcpy(&s.pe, pe + at * 8, 8);
-    };
-    auto use = [&](const Step& s) __attribute__((always_inline)) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < NC; ++i)
-          acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              operand(s.w[i][h]), operand(s.p[h]), acc[i], kFmtE2M1, kFmtE2M1, 0, (h ? s.qe[i].y : s.qe[i].x) >> (8 * g), 0,
-              (h ? s.pe.y : s.pe.x) >> (8 * g));
-    };
-    const int n = ld / 128;  // whole steps
-    Step s[D];
-    if (n > 0) {
-#pragma unroll
-      for (int d = 0; d < D; ++d) load(s[d], min(d, n - 1));
-      int k = 0;
-      for (; k + D <= n; k += D) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-          use(s[d]);
-          load(s[d], min(k + d + D, n - 1));  // (the last ones again where there are no more)
-        }
-      }
-#pragma unroll
-      for (int d = 0; d < D; ++d)
-        if (k + d < n) use(s[d]);
-    }
-    const int left = nb - n * 8;  // the rest of K: 1 to 7 blocks, zeros behind them
-    if (left) {
-      auto rest = [&](const uint8_t* p, int h) __attribute__((always_inline)) {
-        return 4 * h + g < left ? *reinterpret_cast<const v4i*>(p + n * 128 + 64 * h) : v4i{0, 0, 0, 0};
-      };
-      auto rest_scales = [&](const uint8_t* p) __attribute__((always_inline)) {
-        uint2 v = make_uint2(0, 0);  // this lane's two, where the shift of `use` finds them
-        if (g < left) v.x = uint32_t(p[n * 8 + g]) << (8 * g);
-        if (4 + g < left) v.y = uint32_t(p[n * 8 + 4 + g]) << (8 * g);
-        return v;
-      };
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        s[0].w[i][0] = rest(pw[i], 0);
-        s[0].w[i][1] = rest(pw[i], 1);
-        s[0].qe[i] = rest_scales(qe[i]);
-      }
-      s[0].p[0] = rest(pp, 0);
-      s[0].p[1] = rest(pp, 1);
-      s[0].pe = rest_scales(pe);
-      use(s[0]);
-    }
-  }
-  // lane l holds columns 4 (l / 16) + 0..3 of row l % 16 of each fragment
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int c = n0 + i * 16 + 4 * g;
-    if (m < pl.rows && c < a.N)
-      store4(a.out, (long(pl.row0) + m) * a.N + c, t < 0 ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : acc[i], a.out_ty);
   }
 }
 
@@ -791,38 +700,53 @@ __global__ __launch_bounds__(kThreads, 1) void k_mx4(Mx4Args a) {
 }
 
 // The shape of a launch: rows and columns of a tile, and the kernel that makes it.
-enum { kBig, kFew, kDirect };
+enum { kBig, kFew, kRows };  // k_mx4; k_mx4_few with WK = 4; with WK = 1
 struct TileShape {
   int kind, rows, cols;
 };
 
-// The shape that is expected to take the least time, in us: rounds of one tile per CU,
-// each a fixed time plus the bytes of its rows and columns at a rate, both as measured per
-// kernel.  (Calls of one matrix, K = N = 4096, us: 64 rows in 32 x 32 tiles 14.1, 16 x 32 14.8,
-// 64 x 64 15.0; 600 rows in 128 x 256 21, 64 x 64 28, 256 x 256 29; 2048 rows 26, 70, 33.  Top-8
-// of 64: 61 tokens, 2048 -> 7168, direct 112, 128 x 256 113, 16 x 64 147; 512 -> 2048: 18, 19, 61;
-// 512 tokens, 4096 -> 1536: 128 x 256 58, 256 x 256 68, 64 x 64 93; 1024 tokens, 2048 -> 1408: 256
-// x 256 43, 128 x 256 45.  About 10 us of each are the call's.)
+// The shape that is expected to take the least time.  A launch takes a start and its rounds
+// of as many tiles as the CUs hold; a round what a tile takes by itself (its
+// turn, and its K steps one after the other) or what its bytes take through a CU,
+// whichever is more.  The numbers, in us, are fitted to the 17 shapes' times on 33 products
+// (1 to 32768 rows in 1 to 128 groups, K 256 to 16384, N 128 to 7168): the shape that
+// is chosen is the fastest of them in 31, and 3 % slower in two.
+//   us, fastest and others: one row, 7168 -> 4096: kFew 16 x 16 7.0, 16 x 64 12.9; 600 rows, 4096 ->
+//   4096: kBig 128 18.8, 256 27.6, kFew 64 x 64 25.8, kRows 64 x 128 29.5; top-8 of 64: 61
+//   tokens, 2048 -> 7168: kRows 16 x 128 86.8, kBig 128 109.5; 512 tokens, 4096 -> 1536: kBig 128
+//   56.7, 256 64.9, kRows 32 x 256 85.3; 4096 tokens: kBig 256 145, 128 176.
 // The row tiles of ragged groups are estimated: groups with a row, each half a tile more
 // than its mean needs.
 TileShape shape_of(const Mx4Args& a, double* cost_of = nullptr) {
   struct Cost {
-    double fixed, rate;
+    double start, turn, step, rate;  // us, us, us per step of a wave, bytes per us and CU
   };
-  static const Cost cost_of_kind[] = {{10, 40e3}, {4.5, 45e3}, {2, 21e3}};
-  static const TileShape shapes[] = {{kFew, 16, 64}, {kFew, 16, 32}, {kFew, 16, 16}, {kFew, 32, 32}, {kFew, 32, 64},
-                                     {kFew, 32, 16}, {kFew, 64, 64}, {kFew, 64, 32}, {kFew, 64, 16},
-                                     {kDirect, 16, 4 * kDirectCols}, {kBig, 128, kBN}, {kBig, 256, kBN}};
+  static const Cost cost_of_kind[] = {{0, 11, 0.85, 35e3}, {5, 0.8, 1.05, 31e3}, {0.4, 2.8, 0.72, 40e3}};
+  struct Shape {
+    TileShape s;
+    int share;  // workgroups that a CU holds
+  };
+  static const Shape shapes[] = {{{kFew, 16, 16}, 2}, {{kFew, 16, 32}, 2}, {{kFew, 16, 64}, 1}, {{kFew, 32, 16}, 2},
+                                 {{kFew, 32, 32}, 2}, {{kFew, 32, 64}, 1}, {{kFew, 64, 16}, 1}, {{kFew, 64, 32}, 1},
+                                 {{kFew, 64, 64}, 1}, {{kRows, 16, 64}, 4}, {{kRows, 16, 128}, 2},
+                                 {{kRows, 16, 256}, 1}, {{kRows, 32, 128}, 2}, {{kRows, 32, 256}, 1},
+                                 {{kRows, 64, 128}, 1}, {{kBig, 128, kBN}, 1}, {{kBig, 256, kBN}, 1}};
   const double groups = a.E * (1.0 - std::exp(-double(a.R) / a.E));  // that are touched
   const double mean = a.R / std::fmax(groups, 1.0), bytes = a.K / 2.0 + a.K / 32.0;
-  TileShape best = shapes[0];
+  TileShape best = {kBig, 256, kBN};
   double least = 1e300;
-  for (const TileShape& s : shapes) {
-    const double need = mean / s.rows;
-    const double rows = a.E == 1 ? std::ceil(a.R / double(s.rows)) : groups * std::fmax(1.0, need + 0.5);
+  for (const Shape& shape : shapes) {
+    const TileShape& s = shape.s;
     const Cost& c = cost_of_kind[s.kind];
-    const double cost = std::ceil(std::ceil(rows) * std::ceil(double(a.N) / s.cols) / kCUs) *
-                        (c.fixed + (s.rows + s.cols) * bytes / c.rate);
+    const double rows = a.E == 1 ? std::ceil(a.R / double(s.rows)) : groups * std::fmax(1.0, mean / s.rows + 0.5);
+    const double tiles = std::ceil(rows) * std::ceil(double(a.N) / s.cols);
+    const double rounds = std::ceil(tiles / (kCUs * shape.share));
+    // (a step of the large tiles takes as long as they have rows, and a bit; the others' four
+    // waves have a quarter of the steps each, or all)
+    const double steps = std::ceil(a.K / 256.0) * (s.kind == kBig ? s.rows / 256.0 + 0.3 : s.kind == kFew ? 0.25 : 1.0);
+    const double turns = s.kind == kBig ? rounds : tiles / kCUs;
+    const double cost =
+        c.start + std::fmax(rounds * (c.turn + steps * c.step), turns * (s.rows + s.cols) * bytes / c.rate);
     if (cost < least) {
       least = cost;
       best = s;
@@ -867,24 +791,34 @@ int first_rows(const Mx4Args& a) {
 hipError_t launch_one(const Mx4Args& a, const TileShape& s, long grid, hipStream_t st) {
   static_assert(kThreads == kFewWaves * 64, "one limit of a launch");
   if (grid == 0) return hipSuccess;
-  if (s.kind == kDirect) {
-    hipLaunchKernelGGL((k_mx4_direct<3>), dim3(unsigned(grid)), dim3(kThreads), 0, st, a);
-    return hipGetLastError();
-  }
   if (s.kind == kBig) {
     if (s.rows == 256) hipLaunchKernelGGL((k_mx4<256>), dim3(unsigned(grid)), dim3(kThreads), 0, st, a);
     else hipLaunchKernelGGL((k_mx4<128>), dim3(unsigned(grid)), dim3(kThreads), 0, st, a);
     return hipGetLastError();
   }
-#define MOE_FEW(NT, NC)                                                                                          \
-  case NT * 16 + NC:                                                                                             \
-    hipLaunchKernelGGL((k_mx4_few<NC, NT, NT * NC == 1 ? 4 : 2>), dim3(unsigned(grid)), dim3(kFewWaves * 64), 0, \
-                       st, a);                                                                                   \
-    break;
+#define MOE_FEW(NC, NT, S, WK) \
+  hipLaunchKernelGGL((k_mx4_few<NC, NT, S, WK>), dim3(unsigned(grid)), dim3(kThreads), 0, st, a)
+  if (s.kind == kRows) {
+    switch (s.rows + s.cols / 64) {
+      case 17: MOE_FEW(1, 1, 2, 1); break;
+      case 18: MOE_FEW(2, 1, 2, 1); break;
+      case 20: MOE_FEW(4, 1, 2, 1); break;
+      case 34: MOE_FEW(2, 2, 2, 1); break;
+      case 36: MOE_FEW(4, 2, 2, 1); break;
+      case 66: MOE_FEW(2, 4, 2, 1); break;
+    }
+    return hipGetLastError();
+  }
   switch (s.rows + s.cols / 16) {
-    MOE_FEW(1, 1) MOE_FEW(1, 2) MOE_FEW(1, 4)
-    MOE_FEW(2, 1) MOE_FEW(2, 2) MOE_FEW(2, 4)
-    MOE_FEW(4, 1) MOE_FEW(4, 2) MOE_FEW(4, 4)
+    case 17: MOE_FEW(1, 1, 4, 4); break;
+    case 18: MOE_FEW(2, 1, 2, 4); break;
+    case 20: MOE_FEW(4, 1, 2, 4); break;
+    case 33: MOE_FEW(1, 2, 2, 4); break;
+    case 34: MOE_FEW(2, 2, 2, 4); break;
+    case 36: MOE_FEW(4, 2, 2, 4); break;
+    case 65: MOE_FEW(1, 4, 2, 4); break;
+    case 66: MOE_FEW(2, 4, 2, 4); break;
+    case 68: MOE_FEW(4, 4, 2, 4); break;
   }
 #undef MOE_FEW
   return hipGetLastError();
