@@ -989,6 +989,8 @@ def _norm_operands(x, weight, residual, eps, fmt=0, group=0):
 
 
 def _rms_norm(x, weight, residual, eps, out=None, sum_out=None, want_rstd=False):
+    if residual is None and sum_out is not None:
+        raise ValueError("sum_out needs a residual")
     c, R, K, px, pr, pw = _norm_operands(x, weight, residual, eps)
     y, py = _beside("out", out, x)
     s = ps = rstd = None
@@ -1113,6 +1115,8 @@ def moe_rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional
     be x or residual itself.  Not differentiable: operands that need a gradient are refused."""
     _refuse_derivatives("moe_rms_norm_quant", residual, x, weight)
     _refuse_derivatives("moe_rms_norm_quant", sum_out)
+    if residual is None and sum_out is not None:
+        raise ValueError("sum_out needs a residual")
     c, R, K, px, pr, pw = _norm_operands(x, weight, residual, eps, fmt, group)
     dev = x.device
     y = py = s = ps = None

@@ -36,7 +36,8 @@ __global__ __launch_bounds__(256) void k_quant_mx4(const uint16_t* __restrict__ 
       v[u] = up[u] = quant_raw8{0, 0, 0, 0};
       if (i < chunks) {
         const uint16_t* from = x + i * 8;
-        if constexpr (GLU) from += i / row_chunks * K;
+        // (a 32-bit division where it reaches: the 64-bit one costs more than the rest)
+        if constexpr (GLU) from += (chunks < (1L << 32) ? long(uint32_t(i) / uint32_t(row_chunks)) : i / row_chunks) * K;
         v[u] = *reinterpret_cast<const quant_raw8*>(from);
         if constexpr (GLU) up[u] = *reinterpret_cast<const quant_raw8*>(from + K);
       }

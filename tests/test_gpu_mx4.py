@@ -364,6 +364,49 @@ def test_offsets_of_a_longer_array_and_wrong_ones():
     assert not moe.moe_mm_mx4(xq[:0], xs[:0], wq, ws, o, row_token=none).any()  # no token: rows of zeros
 
 
+@pytest.mark.parametrize("R,T,N,K", [(1, 5, 72, 96), (1, 5, 520, 8224), (40, 7, 136, 1056), (300, 1000, 264, 512), (1030, 64, 4096, 1024),
+                                     (4099, 33, 512, 7168)])
+def test_dense_rows_of_tokens(R, T, N, K):
+    """One matrix, rows gathered from tokens, some of which name none: in one launch and in two."""
+    moe = M()
+    g = gen(R + T)
+    wq, ws = moe.moe_quant_mx4(torch.randn(N, K, device=DEV, generator=g).to(BF16))
+    x = torch.randn(T, K, device=DEV, generator=g).to(BF16)
+    rt = torch.randint(0, T, (R,), device=DEV, generator=g, dtype=torch.int32)
+    for bad in (False, True):
+        if bad:
+            rt[::3] = T
+            rt[R // 2] = -7
+        xq, xs = moe.moe_quant_mx4(x)
+        got = moe.moe_mm_mx4(xq, xs, wq, ws, row_token=rt, out_dtype=FP32)
+        live = (rt >= 0) & (rt < T)
+        v = values(xq, xs)[rt.clamp(0, T - 1).long()] * live[:, None]
+        y, mag = reference(v, values(wq, ws)[None], [0, R])
+        near(got, y, mag, K, "gathered")
+        assert not got[~live].any()
+        assert torch.equal(moe.moe_linear_mx4(x, wq, ws, row_token=rt, out_dtype=FP32), got)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with scratch of its own, give what they give alone."""
+    moe = M()
+    g = gen(14)
+    cases = []
+    for R, N, K in ((600, 1032, 2048), (9, 4096, 1056)):
+        wq, ws = moe.moe_quant_mx4(torch.randn(N, K, device=DEV, generator=g).to(BF16))
+        x = torch.randn(R, K, device=DEV, generator=g).to(BF16)
+        cases.append((x, wq, ws, moe.moe_linear_mx4(x, wq, ws)))
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        for st, (x, wq, ws, want) in zip(streams, cases):
+            with torch.cuda.stream(st):
+                got.append((moe.moe_linear_mx4(x, wq, ws), want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in got)
+
+
 def test_streams_and_graph():
     moe = M()
     g = gen(13)

@@ -91,6 +91,8 @@ def test_python_refusals():
         for bad in ((x[0], w), (x.float(), w.float()), (x, w.half()), (x, w[:32]), (x, w, x[:2]), (x, w, x.half())):
             with pytest.raises(ValueError):
                 f(*bad)
+        with pytest.raises(ValueError, match="needs a residual"):
+            f(x, w, sum_out=x)
     with pytest.raises(ValueError, match="no gradient"):
         moe.moe_rms_norm_quant(x, w.clone().requires_grad_())
     with pytest.raises(ValueError, match="where a gradient is needed"):
