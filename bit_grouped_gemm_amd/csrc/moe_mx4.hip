@@ -20,7 +20,7 @@ namespace {
 
 // ------------------------------------------------------------------ quantiser
 // Eight values a lane, four lanes a block.  Bound by HBM: 2 (SwiGLU: 4) bytes in
-// and 17/32 out per value.
+// and 17/32 out per value.  4099 rows of 7168: 12.6 us, 5.9 TB/s.
 constexpr int kQuantUnroll = 4;
 
 template <int TY, bool GLU>
@@ -288,7 +288,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_mx4_few(Mx4Args a) {
 // moe_linear_mx4 for one row: k_mx4_few with the quantiser in front, in every
 // workgroup: its lanes quantise the row while the first weights are on their
 // way; codes and scales stay in LDS, where all K steps read them.  Codes, sums and
-// results are those of the two launches it stands for.
+// results are those of the two launches it stands for.  Bound by latency, the row's and then
+// the weights' (7168 -> 4096: 7.3 us).
 constexpr int kOneChunks = 4;  // chunks of 8 values that a lane has
 constexpr int kOneMaxK = kOneChunks * kFewWaves * 64 * 8;
 
@@ -427,6 +428,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_mx4_one(Mx4Args a) {
 //
 // The 32 x 32 x 64 instruction it is built from issues at twice the rate of the 16 x
 // 16 x 128 one on 4-bit operands (9.7 PFLOP/s against 4.9, nothing else running).
+//
+// Bound by power and the loads into LDS: a step of 256 rows takes 3050 clocks, its matrix
+// instructions 2048 (without its loads 2350, without the instructions 2740), at 1.5 to 1.8 GHz.
+// 4096 x 4096 x 7168: 61 us, 3.9 PFLOP/s; 32768 rows of 64 groups, 4096 -> 1536: 165, 2.5.
 constexpr int kThreads = 256;
 constexpr int kBN = 256;
 
