@@ -941,7 +941,7 @@ def moe_layer_mm(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Te
                  ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """out [T, H] = sum over j of topk_weights[t, j] * w2[e] (silu(g) * u) with (g, u) =
     w1[e] x[t] and e = topk_ids[t, j], for up to 64 tokens: the whole expert layer on
-    16-bit row-major weights in two launches.
+    16-bit row-major weights in two launches (three where that pays).
 
     x [T, H], w1 [E, 2 I, H] (gate rows first) and w2 [E, H, I] are all bfloat16 or all
     float16; topk_ids int32 and topk_weights float32 [T, topk] as moe_route gives

@@ -23,9 +23,10 @@ struct FewArgs {
   int2* tiles;           // [row tiles]: expert, rows
   int32_t* slots;        // [row tiles][kFewTokens]
   uint16_t *hi, *lo;     // [T * k][I]: h as the sum of two 16-bit values
+  float* partial;        // sums of the second product, where workgroups share columns
 };
 
-size_t few_bytes(int T, int I, int E, int k);
+size_t few_bytes(int T, int H, int I, int E, int k);
 void few_carve(FewArgs& a, void* ws);
 hipError_t launch_few(const FewArgs& a, hipStream_t st);
 

@@ -25,7 +25,7 @@ extern "C" int moe_layer_mm_workspace_size(const moe_few_cfg* cfg, size_t* bytes
   if (!cfg || !bytes) return MOE_ERR_NULL_ARG;
   const int rc = check_few(cfg);
   if (rc) return rc;
-  *bytes = cfg->T ? few_bytes(cfg->T, cfg->I, cfg->E, cfg->topk) : 0;
+  *bytes = cfg->T ? few_bytes(cfg->T, cfg->H, cfg->I, cfg->E, cfg->topk) : 0;
   return MOE_OK;
 }
 
@@ -40,7 +40,7 @@ extern "C" int moe_layer_mm(const moe_few_cfg* cfg, const void* x, const int32_t
   if ((rc = check_few(cfg))) return rc;
   if ((rc = misaligned_ptrs({x, w1, w2, out, ws}, {topk_ids, reinterpret_cast<const int32_t*>(topk_weights)}))) return rc;
   if (!some) return MOE_OK;
-  if (ws_bytes < few_bytes(cfg->T, cfg->I, cfg->E, cfg->topk)) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < few_bytes(cfg->T, cfg->H, cfg->I, cfg->E, cfg->topk)) return MOE_ERR_WORKSPACE;
   FewArgs a{};
   a.x = x; a.ids = topk_ids; a.weights = topk_weights; a.w1 = w1; a.w2 = w2; a.out = out;
   a.T = cfg->T; a.H = cfg->H; a.I = cfg->I; a.E = cfg->E; a.k = cfg->topk; a.ty = cfg->dtype;

@@ -460,8 +460,8 @@ int moe_linear_mx4(const moe_mm_cfg* cfg, const void* x, int swiglu, const uint8
 
 /* ------------------------------------------------------------------------
  * The whole expert layer for a FEW tokens on 16-bit ROW-MAJOR weights (experts
- * that are not quantised), in two launches and without a permuted copy of the
- * tokens:
+ * that are not quantised), in two launches (three where that pays) and without
+ * a permuted copy of the tokens:
  *   out[t] = sum over j of topk_weights[t][j] * W2[e] (silu(g) * u),
  *   (g, u) = W1[e] x[t],  e = topk_ids[t][j]
  * fp32 sums, out rounded once.  Between the products h = silu(g) * u is kept as

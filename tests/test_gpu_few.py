@@ -239,3 +239,62 @@ def test_streams_and_graph():
         torch.cuda.synchronize()
         got = out.clone()
         assert torch.equal(got, moe.moe_layer_mm(x, ids, tw, w1, w2)), k
+
+
+# widths whose columns leave CUs idle, with work enough that workgroups share them; k slots, eight waves and the
+# workgroups of a column (8 at most here) are within the 48 roundings of `reference`
+SHARED = [(1, 8, 8, 1024, 4096), (8, 8, 32, 2048, 512), (8, 3, 9, 520, 4000), (9, 8, 16, 2056, 520), (40, 8, 16, 2048, 512),
+          (64, 4, 64, 1000, 328), (64, 32, 40, 1024, 264), (19, 8, 8, 12296, 264)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("T,k,E,H,I", SHARED)
+def test_shared_columns(T, k, E, H, I, dtype):
+    moe = M()
+    note("test_shared_columns", T, k, E, H, I, dtype)
+    g = gen(T * 31 + k * 7 + E + H + I)
+    x = rand(g, T, H, dtype=dtype)
+    w1, w2 = rand(g, E, 2 * I, H, dtype=dtype, scale=H ** -0.5), rand(g, E, H, I, dtype=dtype, scale=I ** -0.5)
+    ids, tw = route(g, T, E, k)
+    got = moe.moe_layer_mm(x, ids, tw, w1, w2)
+    check(got, reference(x, ids, tw, w1, w2), "routed")
+    ws = torch.full((moe.moe_layer_mm_workspace_size(T, H, I, E, k),), 255, dtype=torch.uint8, device=DEV)
+    assert torch.equal(moe.moe_layer_mm(x, ids, tw, w1, w2, ws=ws), got)
+    same = ids[:1].expand(T, k).contiguous()
+    check(moe.moe_layer_mm(x, same, tw, w1, w2, ws=ws), reference(x, same, tw, w1, w2), "same")
+    # one slot only, then none: most workgroups have few steps, or none
+    ids = torch.full_like(ids, -1)
+    ids[T // 2, k // 2] = E - 1
+    one = moe.moe_layer_mm(x, ids, tw, w1, w2, ws=ws)
+    check(one, reference(x, ids, tw, w1, w2), "one slot")
+    assert one[T // 2].any() and not one[:T // 2].any() and not one[T // 2 + 1:].any()
+    ids[T // 2, k // 2] = E
+    assert not moe.moe_layer_mm(x, ids, tw, w1, w2, ws=ws).any()
+
+
+def test_shared_columns_in_a_graph():
+    moe = M()
+    g = gen(77)
+    T, k, E, H, I = 40, 8, 16, 2048, 512
+    x, w1, w2 = rand(g, T, H), rand(g, E, 2 * I, H, scale=H ** -0.5), rand(g, E, H, I, scale=I ** -0.5)
+    ids, tw = route(g, T, E, k)
+    out = torch.empty_like(x)
+    ws = torch.empty(moe.moe_layer_mm_workspace_size(T, H, I, E, k), dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        moe.moe_layer_mm(x, ids, tw, w1, w2, out=out, ws=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_layer_mm(x, ids, tw, w1, w2, out=out, ws=ws)
+    for i in range(4):
+        x.copy_(rand(g, T, H))
+        new_ids, new_tw = route(g, T, E, k)
+        ids.copy_(new_ids)
+        tw.copy_(new_tw)
+        want = moe.moe_layer_mm(x, ids, tw, w1, w2)
+        out.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), i
