@@ -109,7 +109,9 @@ __device__ __forceinline__ int wave_scan_sat(int v) {
 // rows or weights, share an L2.  Tiles run over all columns of four row tiles
 // before the next four, of eight where there are eight columns or more
 // (measured with 6, 8 and 16 columns: 4 and 8 are within 2 % of the best of 2,
-// 4, 8 and 16).  Returns false where the id has no tile.
+// 4, 8 and 16).  BY_GROUP: of the row tiles of one group only, so that its weights come
+// into an L2 once.  Returns false where the id has no tile.
+template <bool BY_GROUP = false>
 __device__ __forceinline__ bool find_tile(const MmArgs& a, int BM, int ncol, int id, Place& pl, int& col) {
   const int lane = threadIdx.x & 63;
   const int G = a.E + (a.clear_rest ? 2 : 0);
@@ -137,19 +139,24 @@ __device__ __forceinline__ bool find_tile(const MmArgs& a, int BM, int ncol, int
   const uint32_t t = (id & 7) * per + (id >> 3);
   if (uint32_t(id >> 3) >= per || t >= tiles) return false;
   const uint32_t high = ncol < 8 ? 4 : 8;
-  const uint32_t block = t / (high * ncol), in = t - block * high * ncol;
-  const uint32_t wide = min(high, uint32_t(total) - block * high);  // row tiles of this block of columns
-  col = int(in / wide);
-  const int want = int(block * high + in % wide);
+  int want = int(t / uint32_t(ncol));  // BY_GROUP: a row tile of the same group
+  auto place = [&](uint32_t t, int total) __attribute__((always_inline)) {  // t's column and row tile, of `total` row tiles
+    const uint32_t block = t / (high * ncol), in = t - block * high * ncol;
+    const uint32_t wide = min(high, uint32_t(total) - block * high);  // row tiles of this block of columns
+    col = int(in / wide);
+    return int(block * high + in % wide);
+  };
+  if (!BY_GROUP) want = place(t, total);
   int before = 0;
   for (int e0 = 0; e0 < G; e0 += 64) {
     if (G > 64) scan(e0);  // else as it stands
     const uint64_t past = __ballot(before + incl > want);
     if (past) {
-      const int l = __ffsll((unsigned long long)past) - 1;
-      const int first = before + __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(n, l);
+      const int l = __ffsll((unsigned long long)past) - 1, tiles = __builtin_amdgcn_readlane(n, l);
+      const int first = before + __builtin_amdgcn_readlane(incl, l) - tiles;
+      const int at = BY_GROUP ? place(t - uint32_t(first) * ncol, tiles) : want - first;
       pl.e = e0 + l;
-      pl.row0 = __builtin_amdgcn_readlane(r.x, l) + (want - first) * BM;
+      pl.row0 = __builtin_amdgcn_readlane(r.x, l) + at * BM;
       pl.rows = min(BM, __builtin_amdgcn_readlane(r.y, l) - pl.row0);
       return true;
     }

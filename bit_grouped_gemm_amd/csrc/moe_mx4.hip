@@ -431,7 +431,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_mx4_one(Mx4Args a) {
 //
 // Bound by power and the loads into LDS: a step of 256 rows takes 3050 clocks, its matrix
 // instructions 2048 (without its loads 2350, without the instructions 2740), at 1.5 to 1.8 GHz.
-// 4096 x 4096 x 7168: 61 us, 3.9 PFLOP/s; 32768 rows of 64 groups, 4096 -> 1536: 165, 2.5.
+// 4096 x 4096 x 7168: 60 us, 4.0 PFLOP/s; 32768 rows of 64 groups, 4096 -> 1536: 160, 2.6 (with the tiles
+// in blocks across groups 165, 427 MB from memory and the last cache in the place of 322; 2048 -> 7168 402 in the
+// place of 414; tiles of up to 128 rows in code of their own, and these last: the same).
 constexpr int kThreads = 256;
 constexpr int kBN = 256;
 
@@ -494,7 +496,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_mx4(Mx4Args a) {
   const int ncol = (a.N + kBN - 1) / kBN, ld = a.K / 2, nb = a.K / 32;
   Place pl;
   int ct;
-  if (!find_tile(a, BM, ncol, blockIdx.x, pl, ct)) return;
+  if (!find_tile<true>(a, BM, ncol, blockIdx.x, pl, ct)) return;
   // (one tile of the whole workgroup: its numbers stay in scalar registers)
   pl.e = __builtin_amdgcn_readfirstlane(pl.e);
   pl.row0 = __builtin_amdgcn_readfirstlane(pl.row0);
