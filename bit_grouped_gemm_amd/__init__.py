@@ -1018,17 +1018,39 @@ class _RmsNorm(torch.autograd.Function):
         return (y, s) if ctx.sums else y
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dy, ds=None):
-        s, weight, rstd = ctx.saved_tensors
-        need_x = ctx.needs_input_grad[0] or ctx.needs_input_grad[2]
-        need_w = ctx.needs_input_grad[1]
-        if dy is None:  # only the sum was used: its gradient is x's and the residual's
-            return ds if ctx.needs_input_grad[0] else None, None, ds if ctx.needs_input_grad[2] else None, None
-        dx = torch.empty_like(s) if need_x else None
-        dw = torch.empty_like(weight) if need_w else None
-        _rms_norm_backward(_usable(dy), None if ds is None else _usable(ds), s, rstd, weight, ctx.eps, dx, dw, None)
-        return dx if ctx.needs_input_grad[0] else None, dw, dx if ctx.needs_input_grad[2] else None, None
+        # (the wrapper only matters where a graph of the gradients is asked for, and takes as long as a launch)
+        return (_rms_norm_grads_once if _grad_enabled() else _rms_norm_grads)(ctx, dy, ds)
+
+
+def _rms_norm_grads(ctx, dy, ds):
+    s, weight, rstd = ctx.saved_tensors
+    need_x, need_w, need_r, _ = ctx.needs_input_grad
+    if dy is None:  # only the sum was used: its gradient is x's and the residual's
+        return ds if need_x else None, None, ds if need_r else None, None
+    # (autograd has checked the gradients against y and s, and forward all that is saved)
+    (R, K), dev = s.shape, s.device
+    c = _norm_cfg(R, K, _DT[s.dtype], _DT[weight.dtype], 0, 0, ctx.eps)
+    dy = _usable(dy)
+    if ds is not None:
+        ds = _usable(ds)
+    dx = dw = work = None
+    need = 0
+    if need_x or need_r:
+        dx = torch.empty_like(s)
+    if need_w:
+        dw = torch.empty_like(weight)
+        need = _scratch_bytes("moe_rms_norm_backward_workspace_size", c)
+        if need:
+            work = torch.empty(need, dtype=torch.uint8, device=dev)
+    _call("moe_rms_norm_backward", dev.index, c, dy.data_ptr() or None, None if ds is None else ds.data_ptr() or None,
+          s.data_ptr() or None, rstd.data_ptr() or None, weight.data_ptr() or None,
+          None if dx is None else dx.data_ptr() or None, None if dw is None else dw.data_ptr() or None,
+          None if work is None else work.data_ptr(), need)
+    return dx if need_x else None, dw, dx if need_r else None, None
+
+
+_rms_norm_grads_once = torch.autograd.function.once_differentiable(_rms_norm_grads)
 
 
 def _usable(dy):

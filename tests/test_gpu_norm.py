@@ -492,3 +492,26 @@ def test_streams_and_graph():
         eager = step()
         torch.cuda.synchronize()
         assert all(torch.equal(u, v) for u, v in zip(got, eager)), k
+
+
+@pytest.mark.parametrize("residual", [False, True])
+def test_a_graph_of_the_gradients_is_refused(residual):
+    """Gradients asked for with create_graph are the same, and have none of their own."""
+    moe = M()
+    g = gen(5)
+    x, w, dy = rand(g, 9, 264), rand(g, 264), rand(g, 9, 264)
+    leaves = [t.requires_grad_() for t in ([x, w, rand(g, 9, 264)] if residual else [x, w])]
+
+    def grads(dy, **kw):
+        out = moe.moe_rms_norm(*leaves)
+        return torch.autograd.grad(out[0] if residual else out, leaves, dy, **kw)
+
+    plain, graph = grads(dy), grads(dy, create_graph=True)
+    for a, b in zip(plain, graph):
+        assert torch.equal(a, b) and not a.requires_grad
+    with pytest.raises(RuntimeError):
+        graph[0].sum().backward()
+    graph = grads(dy.requires_grad_(), create_graph=True)  # linear in dy, which autograd must not pass over
+    assert all(torch.equal(a, b) for a, b in zip(plain, graph))
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        graph[0].sum().backward()
