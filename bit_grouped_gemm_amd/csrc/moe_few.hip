@@ -19,8 +19,8 @@
 //
 // One bf16 token, 8 of 64 experts, H=4096, I=1408: k_up 31 us, 6.0 TB/s of weights, k_down 17,
 // 5.4 (half lines: 40 and 21; a stream of plain reads reaches 6.9 TB/s).  8 tokens that name each
-// expert once: 212, 7.0 TB/s, and 115, 6.4; 61 tokens, popular experts named more often: 277, 5.3 TB/s, and
-// 148 + 5, as the rows of x and h take their share of what reaches a CU.
+// expert once: 212, 7.0 TB/s, and 115, 6.4; 61 tokens, popular experts named more often: 237 to 277 from
+// process to process, 6.2 to 5.3, and 124 to 148 + 5: the rows of x and h take their share of what reaches a CU.
 #include <cmath>
 
 #include "moe_few.h"
