@@ -21,7 +21,7 @@ namespace {
 // ------------------------------------------------------------------ quantiser
 // Eight values a lane, four lanes a block.  Bound by HBM: 2 (SwiGLU: 4) bytes in
 // and 17/32 out per value.  4099 rows of 7168: 12.6 us, 5.9 TB/s.
-constexpr int kQuantUnroll = 4;
+constexpr int kQuantUnroll = 2;
 
 template <int TY, bool GLU>
 __global__ __launch_bounds__(256) void k_quant_mx4(const uint16_t* __restrict__ x, long chunks, int K,
