@@ -250,7 +250,7 @@ constexpr int kDownWaves = 8;
 // Steps [s0, s1) of a row tile for 8 NW columns of out, added to the wave's own sums
 // by token.
 template <int TY, int NW, int NP, int D>
-__device__ __forceinline__ void down_tile(const FewArgs& a, const int32_t* slots, int e, int rows, int n0, int s0, int s1,
+__device__ __forceinline__ void down_tile(const FewArgs& a, const int* slots, int e, int rows, int n0, int s0, int s1,
                                           float (*sums)[8 * NW]) {
   const int lane = threadIdx.x & 63;
   const uint16_t* w2 = static_cast<const uint16_t*>(a.w2) + long(e) * a.H * a.I + chunk_of();
@@ -259,10 +259,12 @@ __device__ __forceinline__ void down_tile(const FewArgs& a, const int32_t* slots
   for (int i = 0; i < NW; ++i) pw[i] = w2 + long(min(n0 + i * 8 + row_of(), a.H - 1)) * a.I;
   const uint16_t* ph[2 * NP];
   int slot[NP];
+  float weight[NP];
+  const int first = __builtin_amdgcn_readfirstlane(slots[0]);  // (for the rows behind the last)
 #pragma unroll
   for (int j = 0; j < NP; ++j) {
-    const int r = j * 8 + row_of();
-    slot[j] = slots[r < rows ? r : 0];
+    slot[j] = j * 8 + row_of() < rows ? slots[j] : first;
+    weight[j] = a.weights[slot[j]];
     ph[j] = a.hi + long(slot[j]) * a.I + chunk_of();
     ph[NP + j] = a.lo + long(slot[j]) * a.I + chunk_of();
   }
@@ -275,14 +277,13 @@ __device__ __forceinline__ void down_tile(const FewArgs& a, const int32_t* slots
 #pragma unroll
   for (int j = 0; j < NP; ++j) {
     const bool mine = j * 8 + row_of() < rows && !(lane & 1);
-    const float weight = mine ? a.weights[slot[j]] : 0.0f;
     float* to = sums[slot[j] / a.k] + 2 * (lane >> 4);
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
       const float2 y = both_halves(acc[i][j]);
       if (mine) {  // (two rows of a tile may be one token's)
-        __hip_atomic_fetch_add(to + i * 8, weight * y.x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-        __hip_atomic_fetch_add(to + i * 8 + 1, weight * y.y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        __hip_atomic_fetch_add(to + i * 8, weight[j] * y.x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        __hip_atomic_fetch_add(to + i * 8 + 1, weight[j] * y.y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
       }
     }
   }
@@ -298,6 +299,19 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_down(FewArgs a, int ncol) {
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int each = (a.I + kStep - 1) / kStep, count = *a.count;
   const long total = max(long(count) * each, 1L), end = total * ncol * (blockIdx.x + 1) / gridDim.x;
+  struct Tile {
+    int e, rows, slots[MAXP];  // this lane's rows' slots (anything behind the last row)
+  };
+  // (all its loads at once, and a tile ahead: 19 tokens 116 us, 119 with each when it is needed)
+  auto tile_at = [&](int v) __attribute__((always_inline)) {
+    Tile t;
+    const int2 head = a.tiles[v];
+    t.e = head.x;
+    t.rows = head.y;
+#pragma unroll
+    for (int j = 0; j < MAXP; ++j) t.slots[j] = a.slots[(v * MAXP + j) * 8 + row_of()];
+    return t;
+  };
   int turn = 0;
   for (long u = total * ncol * blockIdx.x / gridDim.x; u < end; ++turn) {
     const int ct = int(u / total), n0 = ct * kCols;
@@ -305,15 +319,18 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_down(FewArgs a, int ncol) {
     for (int i = lane; i < a.T * kCols; i += 64) sums[w][i / kCols][i % kCols] = 0.0f;
     int at = from + int(long(upto - from) * w / kDownWaves);
     const int last = count ? from + int(long(upto - from) * (w + 1) / kDownWaves) : at;
+    Tile next = at < last ? tile_at(at / each) : Tile{};
     while (at < last) {
       const int v = at / each, s0 = at - v * each, s1 = min(each, s0 + last - at);
-      const int2 tile = a.tiles[v];
-      const int32_t* slots = a.slots + v * 8 * MAXP;
-      constexpr int D = NW == 2 ? 6 : 3;
-      if (MAXP == 1 || tile.y <= 8) down_tile<TY, NW, 1, D>(a, slots, tile.x, tile.y, n0, s0, s1, sums[w]);
-      else if (MAXP == 2 || tile.y <= 16) down_tile<TY, NW, MAXP < 2 ? 1 : 2, D>(a, slots, tile.x, tile.y, n0, s0, s1, sums[w]);
-      else down_tile<TY, NW, MAXP, 2>(a, slots, tile.x, tile.y, n0, s0, s1, sums[w]);
+      const Tile now = next;
       at += s1 - s0;
+      if (at < last) next = tile_at(v + 1);
+      const int e = __builtin_amdgcn_readfirstlane(now.e), rows = __builtin_amdgcn_readfirstlane(now.rows);
+      constexpr int D = NW == 2 ? 6 : 3;
+      if (MAXP == 1 || rows <= 8) down_tile<TY, NW, 1, D>(a, now.slots, e, rows, n0, s0, s1, sums[w]);
+      else if (MAXP == 2 || rows <= 16)
+        down_tile<TY, NW, MAXP < 2 ? 1 : 2, D>(a, now.slots, e, rows, n0, s0, s1, sums[w]);
+      else down_tile<TY, NW, MAXP, 2>(a, now.slots, e, rows, n0, s0, s1, sums[w]);
     }
     __syncthreads();
     const bool whole = from == 0 && upto == total;
