@@ -123,7 +123,7 @@ __device__ __forceinline__ float2 both_halves(const v4f& acc) {
 // 132; 2, 1, 1 306 and 150.  32 columns a workgroup, which halves the reads of x: 290 and 145, as its
 // registers leave one wave per SIMD.  One token, steps: 2 31.2, 3 30.8, 6 30.6, 8 35.)
 constexpr int kUpWaves = 4, kUpCols = 16;
-constexpr int kMaxExperts = 1024;
+constexpr int kMaxExperts = 1024, kMaxTopk = 32;
 
 // 16 columns of h for one row tile: their gate and up rows of W1, K split over the
 // waves, whose sums meet in LDS.
@@ -194,6 +194,7 @@ __global__ __launch_bounds__(kUpWaves * 64, 3) void k_up(FewArgs a, int ncol) {
   constexpr int kRows = 8 * MAXP;
   __shared__ int hist[kMaxExperts];
   __shared__ int list[kRows];
+  __shared__ int16_t named[kFewTokens * kMaxTopk];  // a slot's expert, or -1
   __shared__ float2 part[kUpWaves * (kUpCols / 4) * MAXP * 64];
   const int lane = threadIdx.x & 63, n = a.T * a.k;
   const int want = int(blockIdx.x) / ncol, ct = int(blockIdx.x) - want * ncol;
@@ -201,7 +202,9 @@ __global__ __launch_bounds__(kUpWaves * 64, 3) void k_up(FewArgs a, int ncol) {
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kUpWaves * 64) {
     const int id = a.ids[i];
-    if (id >= 0 && id < a.E) atomicAdd(&hist[id], 1);
+    const bool live = id >= 0 && id < a.E;
+    named[i] = int16_t(live ? id : -1);
+    if (live) atomicAdd(&hist[id], 1);
   }
   __syncthreads();
   // tile `want`: expert e and the rows of its tiles before (every wave by itself)
@@ -224,7 +227,7 @@ __global__ __launch_bounds__(kUpWaves * 64, 3) void k_up(FewArgs a, int ncol) {
   if (e < 0) return;
   if (threadIdx.x < 64) {
     for (int i0 = 0, seen = 0; i0 < n; i0 += 64) {
-      const bool mine = i0 + lane < n && a.ids[i0 + lane] == e;
+      const bool mine = i0 + lane < n && named[i0 + lane] == e;
       const uint64_t all = __ballot(mine);
       const int at = seen + __popcll(all & ((1ull << lane) - 1)) - skip;
       if (mine && at >= 0 && at < rows) {
