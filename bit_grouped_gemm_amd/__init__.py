@@ -1013,9 +1013,9 @@ class _RmsNorm(torch.autograd.Function):
     def forward(ctx, x, weight, residual, eps):
         ctx.set_materialize_grads(False)
         y, s, rstd = _rms_norm(x, weight, residual, eps, want_rstd=True)
-        ctx.eps, ctx.sums = eps, residual is not None
-        ctx.save_for_backward(s if ctx.sums else x, weight, rstd)
-        return (y, s) if ctx.sums else y
+        ctx.eps, ctx.saw = eps, (x.shape, x.dtype, weight.dtype, x.device)
+        ctx.save_for_backward(x if residual is None else s, weight, rstd)
+        return y if residual is None else (y, s)
 
     @staticmethod
     def backward(ctx, dy, ds=None):
@@ -1028,18 +1028,20 @@ def _rms_norm_grads(ctx, dy, ds):
     need_x, need_w, need_r, _ = ctx.needs_input_grad
     if dy is None:  # only the sum was used: its gradient is x's and the residual's
         return ds if need_x else None, None, ds if need_r else None, None
-    # (autograd has checked the gradients against y and s, and forward all that is saved)
-    (R, K), dev = s.shape, s.device
-    c = _norm_cfg(R, K, _DT[s.dtype], _DT[weight.dtype], 0, 0, ctx.eps)
-    dy = _usable(dy)
+    shape, dt, wdt, dev = ctx.saw
+    R, K = shape
+    dy = _back("dy", dy, dt, shape, dev)
     if ds is not None:
-        ds = _usable(ds)
+        ds = _back("the sum's gradient", ds, dt, shape, dev)
+    s, weight = _back("sum", s, dt, shape, dev), _back("weight", weight, wdt, (K,), dev)
+    rstd = _back("rstd", rstd, torch.float32, (R,), dev)
+    c = _norm_cfg(R, K, _DT[dt], _DT[wdt], 0, 0, ctx.eps)
     dx = dw = work = None
     need = 0
     if need_x or need_r:
-        dx = torch.empty_like(s)
+        dx = torch.empty(shape, dtype=dt, device=dev)
     if need_w:
-        dw = torch.empty_like(weight)
+        dw = torch.empty(K, dtype=wdt, device=dev)
         need = _scratch_bytes("moe_rms_norm_backward_workspace_size", c)
         if need:
             work = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -1053,10 +1055,15 @@ def _rms_norm_grads(ctx, dy, ds):
 _rms_norm_grads_once = torch.autograd.function.once_differentiable(_rms_norm_grads)
 
 
-def _usable(dy):
-    """A gradient as the kernels take it: autograd's may be an expanded or an unaligned view."""
-    dy = dy.contiguous()
-    return dy.clone() if dy.data_ptr() % 16 else dy
+def _back(name, t, dtype, shape, dev):
+    """A tensor that autograd hands to a backward pass, as the kernels take it.  It need not be
+    the one that forward saw: a hook may have made another of it, or its data may have been
+    replaced, and a gradient may be an expanded or an unaligned view."""
+    if t.dtype != dtype or t.shape != shape or t.device != dev:
+        raise ValueError(f"moe_rms_norm's gradient: {name} is {t.dtype} {tuple(t.shape)} on {t.device} now, "
+                         f"was {dtype} {tuple(shape)} on {dev}")
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
 
 
 def _rms_norm_backward(dy, dsum, s, rstd, weight, eps, dx, dw, work):
