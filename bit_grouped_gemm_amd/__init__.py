@@ -39,6 +39,7 @@ from __future__ import annotations
 import ctypes as C
 import dataclasses
 import functools
+import operator
 import os
 from typing import Optional, Tuple
 
@@ -796,20 +797,32 @@ def _beside(name, given, like):
     return given, _addr(name, given, (like.dtype,), like.shape, like.device)
 
 
-# The calls' structs, by their values: put together once per shape.
+# The calls' structs, by their values: put together once per shape.  The values are Python's own numbers
+# (a tensor would be kept as itself, with the number it had at first).
+_int = operator.index
+
+
+def _struct(kind, values):
+    c = kind(*values)
+    for (name, ctype), v in zip(kind._fields_, values):
+        if ctype is C.c_int32 and getattr(c, name) != v:
+            raise ValueError(f"{name}: {v} does not fit 32 bits")
+    return C.byref(c)
+
+
 @functools.lru_cache(maxsize=1024)
 def _mm_cfg(*values):
-    return C.byref(MoeMmCfg(*values))
+    return _struct(MoeMmCfg, values)
 
 
 @functools.lru_cache(maxsize=1024)
 def _few_cfg(*values):
-    return C.byref(MoeFewCfg(*values))
+    return _struct(MoeFewCfg, values)
 
 
 @functools.lru_cache(maxsize=1024)
 def _norm_cfg(*values):
-    return C.byref(MoeNormCfg(*values))
+    return _struct(MoeNormCfg, values)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -895,6 +908,7 @@ def moe_mm_mx4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.T
 def moe_linear_mx4_workspace_size(rows: int, K: int, out_rows: Optional[int] = None) -> int:
     """Bytes of scratch moe_linear_mx4 needs for x of `rows` rows, K inputs of w
     and, with row_token, `out_rows` rows of the result."""
+    rows, K, out_rows = _int(rows), _int(K), None if out_rows is None else _int(out_rows)
     return _scratch_bytes("moe_linear_mx4_workspace_size",
                           _mm_cfg(rows if out_rows is None else out_rows, 8, K, 1, rows, 0, 0, 0),
                           int(out_rows is not None))
@@ -933,7 +947,7 @@ def moe_linear_mx4(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, offsets:
 # ------------------------------------------------------------------ the layer for a few tokens
 def moe_layer_mm_workspace_size(T: int, H: int, I: int, E: int, topk: int) -> int:
     """Bytes of scratch moe_layer_mm needs for T tokens."""
-    return _scratch_bytes("moe_layer_mm_workspace_size", _few_cfg(T, H, I, E, topk, 0))
+    return _scratch_bytes("moe_layer_mm_workspace_size", _few_cfg(*map(_int, (T, H, I, E, topk)), 0))
 
 
 def moe_layer_mm(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor, w1: torch.Tensor,
@@ -1086,7 +1100,7 @@ def _rms_norm_backward(dy, dsum, s, rstd, weight, eps, dx, dw, work):
 
 def moe_rms_norm_backward_workspace_size(R: int, K: int) -> int:
     """Bytes of scratch moe_rms_norm_backward needs for the gradient of the weight."""
-    return _scratch_bytes("moe_rms_norm_backward_workspace_size", _norm_cfg(R, K, 0, 0, 0, 0, 1.0))
+    return _scratch_bytes("moe_rms_norm_backward_workspace_size", _norm_cfg(_int(R), _int(K), 0, 0, 0, 0, 1.0))
 
 
 def moe_rms_norm_backward(dy: torch.Tensor, dsum: Optional[torch.Tensor], sum: torch.Tensor, rstd: torch.Tensor,
@@ -1100,7 +1114,7 @@ def moe_rms_norm_backward(dy: torch.Tensor, dsum: Optional[torch.Tensor], sum: t
     _refuse_derivatives("moe_rms_norm_backward", dsum, dy, sum)
     _refuse_derivatives("moe_rms_norm_backward", None, rstd, weight)
     dx, dw = torch.empty_like(sum), torch.empty_like(weight)
-    _rms_norm_backward(dy, dsum, sum, rstd, weight, eps, dx, dw, work)
+    _rms_norm_backward(dy, dsum, sum, rstd, weight, float(eps), dx, dw, work)
     return dx, dw
 
 
@@ -1119,6 +1133,7 @@ def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
     or `sum_out`).  Operands with a forward-mode tangent are refused.  In a
     graph, capture forward and backward together, while no earlier result computed
     from the same leaves is kept."""
+    eps = float(eps)
     if forward_ad._current_level >= 0:
         _refuse_tangents("moe_rms_norm", x, weight, residual, out, sum_out)
     if _grad_enabled():
@@ -1146,7 +1161,8 @@ def moe_rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional
     _refuse_derivatives("moe_rms_norm_quant", sum_out)
     if residual is None and sum_out is not None:
         raise ValueError("sum_out needs a residual")
-    c, R, K, px, pr, pw = _norm_operands(x, weight, residual, eps, fmt, group)
+    fmt, group = _int(fmt), _int(group)
+    c, R, K, px, pr, pw = _norm_operands(x, weight, residual, float(eps), fmt, group)
     dev = x.device
     y = py = s = ps = None
     if want_y:
