@@ -1042,6 +1042,8 @@ def _rms_norm_grads(ctx, dy, ds):
     need_x, need_w, need_r, _ = ctx.needs_input_grad
     if dy is None:  # only the sum was used: its gradient is x's and the residual's
         return ds if need_x else None, None, ds if need_r else None, None
+    if forward_ad._current_level >= 0:
+        _refuse_tangents("moe_rms_norm's gradient", dy, ds)
     shape, dt, wdt, dev = ctx.saw
     R, K = shape
     dy = _back("dy", dy, dt, shape, dev)
