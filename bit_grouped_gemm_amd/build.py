@@ -12,8 +12,9 @@ LIB = os.path.join(BUILD, "libmoe.so")
 SOURCES = ["moe_api.hip", "moe_kernels.hip", "moe_gemm_big.hip", "moe_tile.hip", "moe_diag.hip", "moe_router.hip",
            "moe_mm_api.hip", "moe_mm.hip", "moe_quant_i8.hip", "moe_norm_api.hip", "moe_norm.hip",
            "moe_mx4_api.hip", "moe_mx4.hip", "moe_few_api.hip", "moe_few.hip"]
-HEADERS = ["moe_device.h", "moe_launch.h", "moe_mm.h", "moe_mm_tile.h", "moe_quant_i8.h", "moe_check.h", "moe_norm.h", "moe_quant_mx4.h", "moe_mx4.h", "moe_few.h",
-            os.path.join("..", "..", "include", "moe.h")]
+HEADERS = ["moe_device.h", "moe_launch.h", "moe_mm.h", "moe_mm_tile.h", "moe_quant_i8.h", "moe_check.h",
+           "moe_norm.h", "moe_quant_mx4.h", "moe_mx4.h", "moe_mx4_shape.h", "moe_few.h",
+           os.path.join("..", "..", "include", "moe.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

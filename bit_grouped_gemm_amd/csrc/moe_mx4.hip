@@ -13,6 +13,7 @@
 
 #include "moe_mm_tile.h"
 #include "moe_mx4.h"
+#include "moe_mx4_shape.h"
 #include "moe_quant_mx4.h"
 
 namespace moe {
@@ -436,7 +437,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_mx4_one(Mx4Args a) {
 // in blocks across groups 165, 427 MB from memory and the last cache in the place of 322; 2048 -> 7168 402 in the
 // place of 414; tiles of up to 128 rows in code of their own, and these last: the same).
 constexpr int kThreads = 256;
-constexpr int kBN = 256;
+constexpr int kBN = kMx4Cols;
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 
@@ -708,106 +709,31 @@ __global__ __launch_bounds__(kThreads, 1) void k_mx4(Mx4Args a) {
   else put_out(std::integral_constant<int, kBf16>{});
 }
 
-// The shape of a launch: rows and columns of a tile, and the kernel that makes it.
-enum { kBig, kFew, kRows };  // k_mx4; k_mx4_few with WK = 4; with WK = 1
-struct TileShape {
-  int kind, rows, cols;
-};
-
-// The shape that is expected to take the least time.  A launch takes a start and its rounds
-// of as many tiles as the CUs hold; a round what a tile takes by itself (its
-// turn, and its K steps one after the other) or what its bytes take through a CU,
-// whichever is more.  The numbers, in us, are fitted to the 17 shapes' times on 33 products
-// (1 to 32768 rows in 1 to 128 groups, K 256 to 16384, N 128 to 7168): the shape that
-// is chosen is the fastest of them in 31, and 3 % slower in two.
-//   us, fastest and others: one row, 7168 -> 4096: kFew 16 x 16 7.0, 16 x 64 12.9; 600 rows, 4096 ->
-//   4096: kBig 128 18.8, 256 27.6, kFew 64 x 64 25.8, kRows 64 x 128 29.5; top-8 of 64: 61
-//   tokens, 2048 -> 7168: kRows 16 x 128 86.8, kBig 128 109.5; 512 tokens, 4096 -> 1536: kBig 128
-//   56.7, 256 64.9, kRows 32 x 256 85.3; 4096 tokens: kBig 256 145, 128 176.
-// The row tiles of ragged groups are estimated: groups with a row, each half a tile more
-// than its mean needs.
-TileShape shape_of(const Mx4Args& a, double* cost_of = nullptr) {
-  struct Cost {
-    double start, turn, step, rate;  // us, us, us per step of a wave, bytes per us and CU
-  };
-  static const Cost cost_of_kind[] = {{0, 11, 0.85, 35e3}, {5, 0.8, 1.05, 31e3}, {0.4, 2.8, 0.72, 40e3}};
-  struct Shape {
-    TileShape s;
-    int share;  // workgroups that a CU holds
-  };
-  static const Shape shapes[] = {{{kFew, 16, 16}, 2}, {{kFew, 16, 32}, 2}, {{kFew, 16, 64}, 1}, {{kFew, 32, 16}, 2},
-                                 {{kFew, 32, 32}, 2}, {{kFew, 32, 64}, 1}, {{kFew, 64, 16}, 1}, {{kFew, 64, 32}, 1},
-                                 {{kFew, 64, 64}, 1}, {{kRows, 16, 64}, 4}, {{kRows, 16, 128}, 2},
-                                 {{kRows, 16, 256}, 1}, {{kRows, 32, 128}, 2}, {{kRows, 32, 256}, 1},
-                                 {{kRows, 64, 128}, 1}, {{kBig, 128, kBN}, 1}, {{kBig, 256, kBN}, 1}};
-  const double groups = a.E * (1.0 - std::exp(-double(a.R) / a.E));  // that are touched
-  const double mean = a.R / std::fmax(groups, 1.0), bytes = a.K / 2.0 + a.K / 32.0;
-  TileShape best = {kBig, 256, kBN};
-  double least = 1e300;
-  for (const Shape& shape : shapes) {
-    const TileShape& s = shape.s;
-    const Cost& c = cost_of_kind[s.kind];
-    const double rows = a.E == 1 ? std::ceil(a.R / double(s.rows)) : groups * std::fmax(1.0, mean / s.rows + 0.5);
-    const double tiles = std::ceil(rows) * std::ceil(double(a.N) / s.cols);
-    const double rounds = std::ceil(tiles / (kCUs * shape.share));
-    // (a step of the large tiles takes as long as they have rows, and a bit; the others' four
-    // waves have a quarter of the steps each, or all)
-    const double steps = std::ceil(a.K / 256.0) * (s.kind == kBig ? s.rows / 256.0 + 0.3 : s.kind == kFew ? 0.25 : 1.0);
-    const double turns = s.kind == kBig ? rounds : tiles / kCUs;
-    const double cost =
-        c.start + std::fmax(rounds * (c.turn + steps * c.step), turns * (s.rows + s.cols) * bytes / c.rate);
-    if (cost < least) {
-      least = cost;
-      best = s;
-    }
-  }
-  if (cost_of) *cost_of = least;
-  return best;
-}
-
-long grid_of(const Mx4Args& a, const TileShape& s) {
+long grid_of(const Mx4Args& a, const Mx4Shape& s) {
   return (row_tiles(a, s.rows) * ((a.N + s.cols - 1) / s.cols) + 7) / 8 * 8;
 }
 
 // The shape and the workgroups of a launch; false where no launch holds them.
-bool plan(const Mx4Args& a, TileShape* s, long* grid) {
-  *s = shape_of(a);
+bool plan(const Mx4Args& a, Mx4Shape* s, long* grid) {
+  *s = mx4_shape(a.R, a.N, a.K, a.E);
   *grid = grid_of(a, *s);
   if (*grid <= max_blocks(kThreads)) return true;
-  *s = {kBig, 256, kBN};
+  *s = {kMx4Big, 256, kBN};
   *grid = grid_of(a, *s);
   return *grid <= max_blocks(kThreads);
 }
 
-// Rows of a dense product's first launch.  Where the last few rows would make the
-// large tiles go one more round, they go into a launch of their own, in the shape
-// that suits them, if that is expected to save the time of a launch.
-constexpr double kLaunchTime = 5;
-int first_rows(const Mx4Args& a) {
-  if (a.offsets || a.R <= 256) return a.R;
-  const int rows = a.R / 256 * 256;
-  if (rows == a.R) return a.R;
-  double one, head, tail;
-  shape_of(a, &one);
-  Mx4Args h = a, t = a;
-  h.R = rows;
-  t.R = a.R - rows;
-  shape_of(h, &head);
-  shape_of(t, &tail);
-  return head + tail + kLaunchTime < one ? rows : a.R;
-}
-
-hipError_t launch_one(const Mx4Args& a, const TileShape& s, long grid, hipStream_t st) {
+hipError_t launch_one(const Mx4Args& a, const Mx4Shape& s, long grid, hipStream_t st) {
   static_assert(kThreads == kFewWaves * 64, "one limit of a launch");
   if (grid == 0) return hipSuccess;
-  if (s.kind == kBig) {
+  if (s.kind == kMx4Big) {
     if (s.rows == 256) hipLaunchKernelGGL((k_mx4<256>), dim3(unsigned(grid)), dim3(kThreads), 0, st, a);
     else hipLaunchKernelGGL((k_mx4<128>), dim3(unsigned(grid)), dim3(kThreads), 0, st, a);
     return hipGetLastError();
   }
 #define MOE_FEW(NC, NT, S, WK) \
   hipLaunchKernelGGL((k_mx4_few<NC, NT, S, WK>), dim3(unsigned(grid)), dim3(kThreads), 0, st, a)
-  if (s.kind == kRows) {
+  if (s.kind == kMx4Rows) {
     switch (s.rows + s.cols / 64) {
       case 17: MOE_FEW(1, 1, 2, 1); break;
       case 18: MOE_FEW(2, 1, 2, 1); break;
@@ -836,17 +762,17 @@ hipError_t launch_one(const Mx4Args& a, const TileShape& s, long grid, hipStream
 }  // namespace
 
 bool mx4_too_large(const Mx4Args& a) {
-  TileShape s;
+  Mx4Shape s;
   long grid;
   return !plan(a, &s, &grid);
 }
 
 hipError_t launch_mx4(const Mx4Args& a, hipStream_t st, bool* too_large) {
-  TileShape s, ts;
+  Mx4Shape s, ts;
   long grid, tail_grid;
   *too_large = !plan(a, &s, &grid);
   if (*too_large) return hipSuccess;
-  const int rows = first_rows(a);
+  const int rows = a.offsets ? a.R : mx4_first_rows(a.R, a.N, a.K);
   if (rows == a.R) return launch_one(a, s, grid, st);
   Mx4Args head = a, tail = a;
   head.R = rows;
