@@ -64,3 +64,27 @@ def test_a_weight_with_other_data_is_refused():
         w.data = other
         with pytest.raises(ValueError, match="weight"):
             torch.autograd.grad(y, w, torch.ones_like(y))
+
+
+@pytest.mark.parametrize("R,K,dtype,weight_dtype", [(1, 8, BF16, BF16), (33, 4096, FP16, FP32), (300, 1032, BF16, FP32),
+                                                    (5, 16384, FP16, FP16), (1003, 264, BF16, BF16)])
+def test_the_entry_point_is_what_autograd_gives(R, K, dtype, weight_dtype):
+    """moe_rms_norm_backward on the forward pass's own sum and rstd, bit for bit."""
+    import bit_grouped_gemm_amd as moe
+    print("test_the_entry_point_is_what_autograd_gives", R, K, dtype, weight_dtype, flush=True)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(R + K)
+    rand = lambda *s: torch.randn(*s, device=DEV, generator=g)
+    x, res, w = rand(R, K).to(dtype).requires_grad_(), rand(R, K).to(dtype), rand(K).to(weight_dtype).requires_grad_()
+    dy, ds = rand(R, K).to(dtype), rand(R, K).to(dtype)
+    y, s = moe.moe_rms_norm(x, w, res, eps=1e-5)
+    rstd = [t for t in y.grad_fn.saved_tensors if t.shape == (R,) and t.dtype == FP32][0]
+    # 48 roundings, as rstd has fewer than y
+    want = 1 / torch.sqrt(s.detach().double().square().mean(1) + 1e-5)
+    assert ((rstd.double() - want).abs() <= 48 * 2.0 ** -24 * want).all()
+    for d in (ds, None):
+        dx, dw = torch.autograd.grad((y, s) if d is not None else y, (x, w), (dy, d) if d is not None else dy,
+                                     retain_graph=True)
+        for work in (None, torch.full((moe.moe_rms_norm_backward_workspace_size(R, K) + 64,), 255, dtype=torch.uint8, device=DEV)):
+            a, b = moe.moe_rms_norm_backward(dy, d, s.detach(), rstd, w.detach(), eps=1e-5, work=work)
+            assert torch.equal(a, dx) and torch.equal(b, dw)
