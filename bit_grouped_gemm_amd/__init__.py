@@ -64,6 +64,7 @@ QFMT_E4M3 = 0  # moe_rms_norm_quant's codes
 QFMT_I8 = 1
 QFMT_MXFP4 = 2
 RATE_E2M1_E2M1 = 16  # moe_mfma_rate's e2m1 x e2m1 operand pair
+RATE_E2M1_E2M1_32 = 17  # the same in the 32x32x64 form
 
 EXPORTS = ("moe_workspace_size", "moe_permute", "moe_grouped_gemm1_swiglu", "moe_grouped_gemm2",
            "moe_combine", "moe_layer", "moe_layer_static", "moe_layer_persistent", "moe_layer_persistent_spin_limit",

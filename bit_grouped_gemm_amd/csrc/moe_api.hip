@@ -545,7 +545,9 @@ int moe_stream_read(const void* buf, size_t bytes, void* sink, size_t sink_bytes
 int moe_mfma_rate(int wfmt, int iters, void* sink, size_t sink_bytes, double* flops, void* stream) {
   if (!sink) return MOE_ERR_NULL_ARG;
   if (misaligned(sink)) return MOE_ERR_MISALIGNED;
-  if (wfmt != MOE_WFMT_FP8_BLOCK && wfmt != MOE_WFMT_MXFP4 && wfmt != MOE_RATE_E2M1_E2M1) return MOE_ERR_UNSUPPORTED;
+  if (wfmt != MOE_WFMT_FP8_BLOCK && wfmt != MOE_WFMT_MXFP4 && wfmt != MOE_RATE_E2M1_E2M1 &&
+      wfmt != MOE_RATE_E2M1_E2M1_32)
+    return MOE_ERR_UNSUPPORTED;
   if (iters < 1 || iters > 65536) return MOE_ERR_BAD_SHAPE;
   if (sink_bytes < 4 * size_t(mfma_rate_grid())) return MOE_ERR_WORKSPACE;
   return hip_status(launch_mfma_rate(wfmt, iters, static_cast<float*>(sink), flops, static_cast<hipStream_t>(stream)));

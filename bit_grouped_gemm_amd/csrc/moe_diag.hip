@@ -13,6 +13,7 @@
 // cannot be dropped.
 #include <algorithm>
 
+#include "../../include/moe.h"
 #include "moe_device.h"
 #include "moe_launch.h"
 
@@ -84,6 +85,38 @@ __global__ __launch_bounds__(kStreamThreads) void k_mfma_rate(uint32_t a_word, u
   }
 }
 
+// The same for the 32x32x64 form, which the large tiles of the row-major MXFP4 product are
+// made of: rounds of kRateAcc32 MFMAs, each of which adds 64 to each of its 16 elements a
+// lane, so that the sum of all of them is 16 * 64 * kRateAcc32 * iters, the value above.
+// (e2m1 x e2m1: 9.6 PFLOP/s in launches of a millisecond, 9.7 in longer ones; the 16x16x128 form 4.9.)
+constexpr int kRateAcc32 = 4;
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+__global__ __launch_bounds__(kStreamThreads) void k_mfma_rate_32(uint32_t word, int iters, float* __restrict__ sink) {
+  const int w = int(word);
+  const v8i a = {w, w, w, w, 0, 0, 0, 0};
+  v16f acc[kRateAcc32];
+#pragma unroll
+  for (int j = 0; j < kRateAcc32; ++j)
+#pragma unroll
+    for (int u = 0; u < 16; ++u) acc[j][u] = 0.0f;
+  for (int i = 0; i < iters; ++i) {
+#pragma unroll
+    for (int j = 0; j < kRateAcc32; ++j)
+      acc[j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, a, acc[j], kFmtE2M1, kFmtE2M1, 0, kUnitScale, 0,
+                                                             kUnitScale);
+  }
+  if (threadIdx.x == 0) {
+    float t = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kRateAcc32; ++j)
+#pragma unroll
+      for (int u = 0; u < 16; ++u) t += acc[j][u];
+    sink[blockIdx.x] = t;
+  }
+}
+
 // The quantisers' fp32 -> e4m3 conversion (enc_e4m3x4: saturation at +-448,
 // round to nearest even, sign kept) on n values, four per thread.
 __global__ __launch_bounds__(kStreamThreads) void k_encode_e4m3(const float* __restrict__ v, long n,
@@ -111,6 +144,8 @@ int mfma_rate_grid() { return stream_read_grid(); }
 
 hipError_t launch_mfma_rate(int wfmt, int iters, float* sink, double* flops, hipStream_t st) {
   const int grid = mfma_rate_grid();
+  // (a round of the 32x32x64 form has as many operations: half as many MFMAs of twice as many)
+  static_assert(kRateAcc * 16 * 16 * 128 == kRateAcc32 * 32 * 32 * 64, "operations of a round");
   if (flops) *flops = double(grid) * (kStreamThreads / kWave) * double(iters) * kRateAcc * (16.0 * 16.0 * 128.0 * 2.0);
   // operands of 1.0: e4m3 0x38 in every byte, e2m1 0x2 in every nibble
   if (wfmt == 0)
@@ -119,6 +154,8 @@ hipError_t launch_mfma_rate(int wfmt, int iters, float* sink, double* flops, hip
   else if (wfmt == 1)
     hipLaunchKernelGGL((k_mfma_rate<kFmtE2M1, kFmtE4M3>), dim3(unsigned(grid)), dim3(kStreamThreads), 0, st,
                        0x22222222u, 0x38383838u, iters, sink);
+  else if (wfmt == MOE_RATE_E2M1_E2M1_32)
+    hipLaunchKernelGGL(k_mfma_rate_32, dim3(unsigned(grid)), dim3(kStreamThreads), 0, st, 0x22222222u, iters, sink);
   else  // e2m1 x e2m1 (MOE_RATE_E2M1_E2M1)
     hipLaunchKernelGGL((k_mfma_rate<kFmtE2M1, kFmtE2M1>), dim3(unsigned(grid)), dim3(kStreamThreads), 0, st,
                        0x22222222u, 0x22222222u, iters, sink);

@@ -562,16 +562,17 @@ int moe_stream_read(const void* buf, size_t bytes, void* sink, size_t sink_bytes
 /* Diagnostic: the issued rate of the scaled 16x16x128 MFMA the GEMMs use,
  * for the operand formats of `wfmt` (MOE_WFMT_FP8_BLOCK: e4m3 x e4m3;
  * MOE_WFMT_MXFP4: e2m1 weights x e4m3 activations; MOE_RATE_E2M1_E2M1:
- * e2m1 x e2m1, the 4-bit-activation layer's GEMMs).  Four workgroups of four
- * waves per CU each run `iters` (1 .. 65536) rounds of eight independent
- * MFMAs on operands that are all 1.0 with unit scales; `sink` (device, at
+ * e2m1 x e2m1, the 4-bit-activation layer's GEMMs), or of the 32x32x64 one
+ * (MOE_RATE_E2M1_E2M1_32: e2m1 x e2m1, the large tiles of moe_mm_mx4).  Four
+ * workgroups of four waves per CU each run `iters` (1 .. 65536) rounds of eight
+ * (32x32x64: four) independent MFMAs on operands that are all 1.0 with unit scales; `sink` (device, at
  * least 16 * CU-count bytes; 4 KiB covers an MI355X) receives one fp32 per
  * workgroup, exactly 4096 * iters.  `*flops` (host, may be NULL) is set to the
- * FLOP count enqueued (2 * 16 * 16 * 128 per MFMA), so FLOP/s = *flops / the
+ * FLOP count enqueued (2 * 16 * 16 * 128 or 2 * 32 * 32 * 64 per MFMA), so FLOP/s = *flops / the
  * call's duration on `stream`.  MOE_ERR_NULL_ARG (sink), MOE_ERR_MISALIGNED,
  * MOE_ERR_UNSUPPORTED (other wfmt), MOE_ERR_BAD_SHAPE (iters) and
  * MOE_ERR_WORKSPACE (sink too small) are host checks. */
-enum { MOE_RATE_E2M1_E2M1 = 16 };  /* not a weight format: the probe's third operand pair */
+enum { MOE_RATE_E2M1_E2M1 = 16, MOE_RATE_E2M1_E2M1_32 = 17 };  /* no weight formats: the probe's further forms */
 int moe_mfma_rate(int wfmt, int iters, void* sink, size_t sink_bytes, double* flops, void* stream);
 
 /* Diagnostic: the fp32 -> e4m3 conversion every quantiser of the layer
