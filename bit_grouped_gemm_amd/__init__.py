@@ -1047,11 +1047,13 @@ def _rms_norm_grads(ctx, dy, ds):
         _refuse_tangents("moe_rms_norm's gradient", dy, ds)
     shape, dt, wdt, dev = ctx.saw
     R, K = shape
-    dy = _back("dy", dy, dt, shape, dev)
+    dy, pd = _back("dy", dy, dt, shape, dev)
+    pg = None
     if ds is not None:
-        ds = _back("the sum's gradient", ds, dt, shape, dev)
-    s, weight = _back("sum", s, dt, shape, dev), _back("weight", weight, wdt, (K,), dev)
-    rstd = _back("rstd", rstd, torch.float32, (R,), dev)
+        ds, pg = _back("the sum's gradient", ds, dt, shape, dev)
+    s, ps = _back("sum", s, dt, shape, dev)
+    weight, pw = _back("weight", weight, wdt, (K,), dev)
+    rstd, pr = _back("rstd", rstd, torch.float32, (R,), dev)
     c = _norm_cfg(R, K, _DT[dt], _DT[wdt], 0, 0, ctx.eps)
     dx = dw = work = None
     need = 0
@@ -1062,8 +1064,7 @@ def _rms_norm_grads(ctx, dy, ds):
         need = _scratch_bytes("moe_rms_norm_backward_workspace_size", c)
         if need:
             work = torch.empty(need, dtype=torch.uint8, device=dev)
-    _call("moe_rms_norm_backward", dev.index, c, dy.data_ptr() or None, None if ds is None else ds.data_ptr() or None,
-          s.data_ptr() or None, rstd.data_ptr() or None, weight.data_ptr() or None,
+    _call("moe_rms_norm_backward", dev.index, c, pd, pg, ps, pr, pw,
           None if dx is None else dx.data_ptr() or None, None if dw is None else dw.data_ptr() or None,
           None if work is None else work.data_ptr(), need)
     return dx if need_x else None, dw, dx if need_r else None, None
@@ -1073,14 +1074,17 @@ _rms_norm_grads_once = torch.autograd.function.once_differentiable(_rms_norm_gra
 
 
 def _back(name, t, dtype, shape, dev):
-    """A tensor that autograd hands to a backward pass, as the kernels take it.  It need not be
+    """A tensor that autograd hands to a backward pass, as the kernels take it, and its address.  It need not be
     the one that forward saw: a hook may have made another of it, or its data may have been
     replaced, and a gradient may be an expanded or an unaligned view."""
     if t.dtype != dtype or t.shape != shape or t.device != dev:
         raise ValueError(f"moe_rms_norm's gradient: {name} is {t.dtype} {tuple(t.shape)} on {t.device} now, "
                          f"was {dtype} {tuple(shape)} on {dev}")
-    t = t.contiguous()
-    return t.clone() if t.data_ptr() % 16 else t
+    p = t.data_ptr()
+    if p % 16 or not t.is_contiguous():
+        t = t.clone(memory_format=torch.contiguous_format)
+        p = t.data_ptr()
+    return t, p or None
 
 
 def _rms_norm_backward(dy, dsum, s, rstd, weight, eps, dx, dw, work):
