@@ -46,3 +46,39 @@ def test_one_row_of_a_wide_projection(K, N, swiglu):
                         moe.moe_mm_mx4(*moe.moe_quant_mx4(x, swiglu), wq, ws, out_dtype=out)):
                 assert got.shape == (1, N) and torch.isfinite(got).all()
                 assert ((got[0].double() - y).abs() <= tol).all(), (K, N, out)
+
+
+@pytest.mark.parametrize("swiglu", [False, True], ids=["plain", "swiglu"])
+def test_one_row_that_is_not_finite_or_of_no_group(swiglu):
+    """A block with an infinity or NaN makes the row NaN; a row of no group, or one that names no token, is zeros
+    whatever x holds, and stays as it is in a caller's tensor."""
+    import bit_grouped_gemm_amd as moe
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    K, N, E = 1344, 264, 3
+    wq = torch.randint(0, 256, (E, N, K // 2), device=DEV, generator=g, dtype=torch.uint8)
+    ws = torch.full((E, N, K // 32), 127, dtype=torch.uint8, device=DEV)
+    x = torch.randn(1, 2 * K if swiglu else K, device=DEV, generator=g).to(BF16)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)
+    clean = moe.moe_linear_mx4(x, wq[1].contiguous(), ws[1].contiguous(), swiglu=swiglu, out_dtype=FP32)
+    assert torch.isfinite(clean).all() and clean.any()
+    assert torch.equal(moe.moe_linear_mx4(x, wq, ws, i32(0, 0, 1, 1), swiglu=swiglu, out_dtype=FP32), clean)
+    for bad in (float("inf"), float("nan")):
+        y = x.clone()
+        y[0, 700] = bad
+        assert moe.moe_linear_mx4(y, wq[1].contiguous(), ws[1].contiguous(), swiglu=swiglu).isnan().all()
+        for o in ((0, 0, 0, 0), (1, 1, 1, 1)):
+            assert not moe.moe_linear_mx4(y, wq, ws, i32(*o), swiglu=swiglu).any()
+            out = torch.full((1, N), 7.0, dtype=BF16, device=DEV)
+            moe.moe_linear_mx4(y, wq, ws, i32(*o), swiglu=swiglu, out=out)
+            assert (out == 7).all()
+        for t in (-1, 1, 1 << 30):
+            assert not moe.moe_linear_mx4(y, wq, ws, i32(0, 0, 1, 1), row_token=i32(t), swiglu=swiglu).any()
+        both = torch.cat([y, x])
+        assert torch.equal(moe.moe_linear_mx4(both, wq, ws, i32(0, 0, 1, 1), row_token=i32(1), swiglu=swiglu, out_dtype=FP32), clean)
+    wn = ws[1].clone()
+    wn[9, 3] = 255
+    y = moe.moe_linear_mx4(x, wq[1].contiguous(), wn, swiglu=swiglu, out_dtype=FP32)
+    assert y[0, 9].isnan() and torch.equal(y[0, :9], clean[0, :9]) and torch.equal(y[0, 10:], clean[0, 10:])
