@@ -960,10 +960,13 @@ def moe_layer_mm(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Te
 
     x [T, H], w1 [E, 2 I, H] (gate rows first) and w2 [E, H, I] are all bfloat16 or all
     float16; topk_ids int32 and topk_weights float32 [T, topk] as moe_route gives
-    them.  Ids outside [0, E) are masked slots.  `ws`: uint8 scratch of at least
+    them.  Ids outside [0, E) are masked slots.  h = silu(g) * u has 17 bits in
+    bfloat16 and 21 in float16, down to 2^-24 there; past float16's 65504 it is
+    infinite, and with it the token's result.  `ws`: uint8 scratch of at least
     moe_layer_mm_workspace_size(...) bytes, allocated where absent; calls that share
     one must not overlap.  An always-on shared expert is one more matrix pair behind
-    the others, named by one more slot of weight 1.  For more tokens use moe_grouped_mm
+    the others, named by one more slot of weight 1 (from 33 tokens on its weights
+    are read twice).  For more tokens use moe_grouped_mm
     (MOE_ERR_UNSUPPORTED here).  Not differentiable: operands that need a gradient are refused."""
     _refuse_derivatives("moe_layer_mm", out, x, topk_weights)
     _refuse_derivatives("moe_layer_mm", None, w1, w2)
@@ -1131,7 +1134,7 @@ def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
     residual; returns y, or (y, s) where there is a residual.
 
     x and residual [R, K] are bfloat16 or float16 (K a multiple of 8 up to
-    16384), weight [K] is of their type or float32.  s is rounded to their type
+    16384), weight [K] is of their type or float32, eps 1e-30 to 1.  s is rounded to their type
     before it is normalised: it is what the residual stream carries on.  `out` and
     `sum_out` receive y and s; `sum_out` may be x or residual itself.  All tensors
     are contiguous and on one GPU.
@@ -1159,7 +1162,8 @@ def moe_rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional
     """moe_rms_norm with quantised rows: (codes, scales, y, sum).
 
     fmt QFMT_E4M3: codes uint8 [R, K] and float32 scales [R, K / group], group 32
-    or 128 (the layer's xq and xs: moe_grouped_gemm1_swiglu takes them); QFMT_I8:
+    or 128 (moe_grouped_gemm1_swiglu takes them for xq and xs; moe_permute, which
+    gives it the rest, quantises all the same); QFMT_I8:
     int8 [R, K] and float32 [R] (moe_mm_i8's); QFMT_MXFP4: uint8 [R, K / 2] and
     [R, K / 32] (moe_mm_mx4's).  y is the 16-bit result, for the router, or None
     without `want_y`; sum is x + residual, or None without a residual.  `sum_out` may

@@ -21,7 +21,7 @@ struct FewArgs {
   // workspace
   int32_t* count;        // row tiles, 1 int
   int2* tiles;           // [row tiles]: expert, rows
-  int32_t* slots;        // [row tiles][kFewTokens]
+  int32_t* slots;        // [row tiles][rows of a tile: 8, 16 or 32]
   uint16_t *hi, *lo;     // [T * k][I]: h as the sum of two 16-bit values
   float* partial;        // sums of the second product, where workgroups share columns
 };

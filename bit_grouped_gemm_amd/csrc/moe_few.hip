@@ -4,11 +4,13 @@
 //   out[t]  = sum over j of weight[t][j] W2 h[t][j]           (k_down, k_down_join)
 // with the matrices of expert id[t][j].
 //
-// Bound by the touched experts' weights, which are read once: lanes load matrix
-// operands straight into registers, several steps ahead, and nothing is shared
-// between waves but their sums.  h stays exact enough for fp32 results: it is
-// kept as the sum of two 16-bit values, and the second product takes both (the
-// matrix units wait for memory here, so the second half costs nothing).
+// Bound by the touched experts' weights, which are read once for each tile of rows (as a
+// rule an expert has one): lanes load matrix operands straight into registers, several
+// steps ahead, and nothing is shared between waves but their sums.  h is kept as the sum of
+// two 16-bit values, and the second product takes both (the matrix units wait for memory
+// here, so the second half costs nothing): 2^-17 of it is lost in bf16, 2^-21 in fp16, where
+// the lower value ends at 2^-24, so that an h below some 2^-14 is an fp16 value, and one past
+// 65504 is infinite.
 //
 // A 16 x 16 x 32 product takes 16 rows of 64 bytes, which is half of each line: the other
 // half then waits in the L1 for the next load, among those of a dozen waves, and is
@@ -19,8 +21,10 @@
 //
 // One bf16 token, 8 of 64 experts, H=4096, I=1408: k_up 31 us, 6.0 TB/s of weights, k_down 17,
 // 5.4 (half lines: 40 and 21; a stream of plain reads reaches 6.9 TB/s).  8 tokens that name each
-// expert once: 212, 7.0 TB/s, and 115, 6.4; 61 tokens, popular experts named more often: 237 to 277 from
-// process to process, 6.2 to 5.3, and 124 to 148 + 5: the rows of x and h take their share of what reaches a CU.
+// expert once: 212, 7.0 TB/s, and 115, 6.4; 61 tokens, popular experts named more often: 231 to 280 from
+// process to process, 6.4 to 5.3, and 122 to 154 + 5: the rows of x and h take their share of what reaches a CU.
+// Rows that are no whole lines (H or I no multiple of 64) cost half as much again and more: 8 tokens, H=4096,
+// I=1408, 45 experts 162 and 83 us, 6.4 and 6.3 TB/s; H=4104, I=1416, 39 experts 226 and 110, 4.0 and 4.1.
 #include <cmath>
 
 #include "moe_few.h"

@@ -21,8 +21,9 @@ namespace {
 
 // ------------------------------------------------------------------ quantiser
 // Eight values a lane, four lanes a block.  Bound by HBM: 2 (SwiGLU: 4) bytes in
-// and 17/32 out per value.  4099 rows of 7168: 12.4 us, 6.0 TB/s (four
-// chunks of a lane in flight 12.8, and with loads past the caches 14.5).
+// and 17/32 out per value.  4099 rows of 7168: 11.9 to 12.4 us, 6.2 to 6.0 TB/s (four
+// chunks of a lane in flight 12.8, and with loads past the caches 14.5).  SwiGLU, 32768 rows of
+// 2 x 2048: 70 us, 4.3 TB/s; 488 rows 4.7, a launch.
 constexpr int kQuantUnroll = 2;
 
 template <int TY, bool GLU>
@@ -100,8 +101,8 @@ __device__ __forceinline__ int token_of(const Mx4Args& a, int row) {
 //     rows (a decode batch's experts): nothing to join, and loads that never pause.
 // Bound by the weights' bytes.  S is 2, which lets the most workgroups share a CU; but for
 // 16 x 16 tiles, which as a rule have a CU to themselves.  (61 tokens, top-8 of 64, us: 7168 ->
-// 2048 75, 6.7 TB/s of weights, with four stages 78, as four quarters 113; 2048 -> 7168 84,
-// 6.0 TB/s.)
+// 2048 75 to 83 from process to process, 6.7 to 6.0 TB/s of weights, with four stages 78 and as
+// four quarters 113 where these take 75; 2048 -> 7168 84 to 98, 6.0 to 5.1 TB/s.)
 constexpr int kFewWaves = 4;
 
 template <int NC, int NT, int S, int WK>
@@ -289,9 +290,12 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_mx4_few(Mx4Args a) {
 
 // moe_linear_mx4 for one row: k_mx4_few with the quantiser in front, in every
 // workgroup: its lanes quantise the row while the first weights are on their
-// way; codes and scales stay in LDS, where all K steps read them.  Codes, sums and
-// results are those of the two launches it stands for.  Bound by latency, the row's and then
-// the weights' (7168 -> 4096: 7.3 us).
+// way; codes and scales stay in LDS, where all K steps read them.  The codes are the
+// quantiser's; sums are put together like those of k_mx4_few with WK = 4, so that a result has
+// the bits of the two launches where these take that form (K past 1280, up to 16384 columns).
+// Bound by latency, the row's and then the weights' (7168 -> 4096: 7.0 to 8.4 us, quantiser and product by
+// themselves 4.8 and 6.6).  Wide products quantise the row in many workgroups, but lose no more than the launch
+// saved: 4096 -> 28672 14.3 us, two launches 4.8 + 11.2; 57344 24.5 to 25.1, 4.8 + 20.2; 151936 57.8, 4.8 + 51.1.
 constexpr int kOneChunks = 4;  // chunks of 8 values that a lane has
 constexpr int kOneMaxK = kOneChunks * kFewWaves * 64 * 8;
 
@@ -433,9 +437,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_mx4_one(Mx4Args a) {
 //
 // Bound by power and the loads into LDS: a step of 256 rows takes 3050 clocks, its matrix
 // instructions 2048 (without its loads 2350, without the instructions 2740), at 1.5 to 1.8 GHz.
-// 4096 x 4096 x 7168: 60 us, 4.0 PFLOP/s; 32768 rows of 64 groups, 4096 -> 1536: 160, 2.6 (with the tiles
-// in blocks across groups 165, 427 MB from memory and the last cache in the place of 322; 2048 -> 7168 402 in the
-// place of 414; tiles of up to 128 rows in code of their own, and these last: the same).
+// 4096 x 4096 x 7168: 60 to 62 us, 4.0 PFLOP/s; 32768 rows of 64 groups, 4096 -> 1536: 155 to 168 from process to
+// process, 2.7 to 2.5 (with the tiles in blocks across groups 165 where these take 160, 427 MB from memory and
+// the last cache in the place of 322; 2048 -> 7168 402 in the place of 414; tiles of up to 128 rows in code of
+// their own, and these last: the same).
 constexpr int kThreads = 256;
 constexpr int kBN = kMx4Cols;
 

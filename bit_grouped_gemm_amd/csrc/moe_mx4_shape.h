@@ -23,7 +23,8 @@ struct Mx4Shape {
 //   us, fastest and others: one row, 7168 -> 4096: Few 16 x 16 7.0, 16 x 64 12.9; 600 rows, 4096 ->
 //   4096: Big 128 18.8, 256 27.6, Few 64 x 64 25.8, Rows 64 x 128 29.5; top-8 of 64: 61
 //   tokens, 2048 -> 7168: Rows 16 x 128 86.8, Big 128 109.5; 512 tokens, 4096 -> 1536: Big 128
-//   56.7, 256 64.9, Rows 32 x 256 85.3; 4096 tokens: Big 256 145, 128 176.
+//   56.7, 256 64.9, Rows 32 x 256 85.3; 4096 tokens: Big 256 145, 128 176.  (Of one process each; from process
+//   to process all of a product's times move together, by up to 15 %.)
 // The row tiles of ragged groups are estimated: groups with a row, each half a tile more
 // than its mean needs.
 inline Mx4Shape mx4_shape(int R, int N, int K, int E, double* cost_of = nullptr) {

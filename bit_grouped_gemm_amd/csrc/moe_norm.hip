@@ -109,10 +109,11 @@ __device__ __forceinline__ uint32_t row_top(uint32_t v, uint32_t* slot) {
 constexpr float kTiny = 0x1p-80f;  // keeps the squares of any finite row's values, and their sum, inside fp32
 
 // THREADS lanes per row (64: four rows per workgroup), NC chunks of 8 values a lane.
-// Bound by HBM: 8 bytes a value with the residual, 16384 rows of 4096: 85 us, 6.3 TB/s.
+// Bound by HBM: 8 bytes a value with the residual, 16384 rows of 4096: 85 to 93 us from process to
+// process, 6.3 to 5.8 TB/s; to int8 codes 83, 5.7, to MXFP4 78, 5.6 (7 and 6.5 bytes a value).
 //
 // Beside codes the sum is stored past the caches, as it is next read when the layer's result is
-// there (4099 rows of 4096 to e4m3: 25 us, 28 through them).  By itself it is not: in front of its own
+// there (4099 rows of 4096 to e4m3: 21 to 25 us, 28 through them where these take 25).  By itself it is not: in front of its own
 // gradients 16384 rows of 4096 take 85 us, 96 past the caches.
 template <int TY, int FMT, int THREADS, int NC>
 __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void k_norm(NormArgs a) {
@@ -228,8 +229,8 @@ int grad_blocks(int R, int K) {
   return int(need < most ? need : most);
 }
 
-// Bound by HBM: 8 bytes a value with the sum's gradient; 16384 rows of 4096: 102 us with the
-// join, 5.3 TB/s.
+// Bound by HBM: 8 bytes a value with the sum's gradient; 16384 rows of 4096: 97 to 111 us from process
+// to process and 5 for the join, 5.3 to 4.6 TB/s.
 template <int TY, int THREADS, int NC>
 __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void k_norm_grad(NormGradArgs a) {
   constexpr int kRows = THREADS < 256 ? 256 / THREADS : 1;

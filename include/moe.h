@@ -465,8 +465,12 @@ int moe_linear_mx4(const moe_mm_cfg* cfg, const void* x, int swiglu, const uint8
  *   out[t] = sum over j of topk_weights[t][j] * W2[e] (silu(g) * u),
  *   (g, u) = W1[e] x[t],  e = topk_ids[t][j]
  * fp32 sums, out rounded once.  Between the products h = silu(g) * u is kept as
- * the sum of two values of dtype (past fp16's range it is infinite).  The weights
- * of an expert that some token names are read once, the others not at all.
+ * the sum of two values of dtype: to 2^-17 of itself in bf16, to 2^-21 in fp16, but
+ * there no finer than 2^-24, and past fp16's range (65504) it is infinite, and the
+ * token's result with it.  An expert's weights are read once for each 8, 16 or 32 of
+ * its rows (T up to 8, up to 16, more), so once as a rule: twice for an expert that
+ * 33 tokens or more name, a shared one say; those of an expert that no token names
+ * are not read at all.
  *
  * moe_few_cfg (host struct): T tokens (0 .. 64), H hidden size and I expert
  *   width (multiples of 8 up to 2^16), E experts (up to 1024), topk slots per
@@ -523,7 +527,10 @@ int moe_rms_norm(const moe_norm_cfg* cfg, const void* x, const void* residual, c
 
 /* The same with y's codes, made from the fp32 values:
  *   MOE_QFMT_E4M3  codes uint8 [R][K], scales fp32 [R][K / group], group 32 or
- *                  128, by the layer's activation rule: moe_permute's xq and xs
+ *                  128, by the layer's activation rule: moe_grouped_gemm1_swiglu
+ *                  takes them for moe_permute's xq and xs (moe_permute, which
+ *                  its row_token and offsets come from, quantises all the same,
+ *                  and moe_layer and its other forms take 16-bit rows only)
  *   MOE_QFMT_I8    codes int8 [R][K], scales fp32 [R], by moe_quant_i8's rule
  *                  (K a multiple of 16): what moe_mm_i8 takes
  *   MOE_QFMT_MXFP4 codes uint8 [R][K / 2], scales uint8 [R][K / 32], by
