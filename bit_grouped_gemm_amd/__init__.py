@@ -617,6 +617,8 @@ class _GroupedMM(torch.autograd.Function):
     def backward(ctx, dy):
         # moe_grouped_mm_dgrad and moe_grouped_mm_wgrad, with one round of checks
         x, w, offsets = ctx.saved_tensors
+        if forward_ad._current_level >= 0:
+            _refuse_tangents("moe_grouped_mm's gradient", dy)
         dy = dy.contiguous()
         if dy.data_ptr() % 16:  # a view into something else
             dy = dy.clone()
